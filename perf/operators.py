@@ -130,7 +130,7 @@ def _doc_lengths(c):
     # two tokens a document at least: where every query has one key alone, the gradients are zero but for rounding
     k = min(max(1, c["docs"]), n // 4 + 1)
     w = [1 + (i * 5 + 3) % (2 * k + 1) for i in range(k)]
-    cut = [0] + [max(2 * i, n * sum(w[:i]) // sum(w)) for i in range(1, k)] + [n]
+    cut = [2 * i + (n - 2 * k) * sum(w[:i]) // sum(w) for i in range(k + 1)]
     return [b - a for a, b in zip(cut, cut[1:])]
 
 
