@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblh.so")
 MAX_LEVELS = 16
@@ -19,6 +19,8 @@ LH_OK = 0
 STATUS_NAMES = {0: "LH_OK", 1: "LH_ERR_INVALID_ARG", 2: "LH_ERR_UNSUPPORTED", 3: "LH_ERR_WORKSPACE",
                 4: "LH_ERR_CUDA", 5: "LH_ERR_TIMEOUT", 6: "LH_ERR_DEVICE"}
 DTYPES = {"bf16": 0, "fp32": 1}
+DENSE_DTYPES = {"bf16": 0, "fp32": 1, "fp16": 2}  # the dense attention, rotary and cache calls
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 SCORERS = {"qk_sum": 0, "k": 1, "q": 2}
 SELECTIONS = {"parents": 0, "direct": 1, "nested": 2}
 
@@ -56,9 +58,24 @@ class LhPisaInfo(ctypes.Structure):
                 ("max_candidates", c_int32)]
 
 
+class LhRotaryConfig(ctypes.Structure):
+    _fields_ = [("B", c_int64), ("N", c_int64), ("Hq", c_int32), ("Hk", c_int32), ("d", c_int32), ("rot", c_int32),
+                ("layout", c_int32), ("dtype", c_int32), ("inverse", c_int32), ("amplitude", c_float),
+                ("q_stride", c_int64 * 3), ("k_stride", c_int64 * 3), ("q_out_stride", c_int64 * 3),
+                ("k_out_stride", c_int64 * 3)]
+
+
+class LhDenseConfig(ctypes.Structure):
+    _fields_ = ([("B", c_int64), ("N", c_int64), ("Hq", c_int32), ("Hkv", c_int32), ("d", c_int32), ("dtype", c_int32),
+                 ("causal", c_int32), ("scale", c_float), ("softcap", c_float)]
+                + [(f"{n}_stride", c_int64 * 3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")])
+
+
 _P = c_void_p
 _CFG = POINTER(LhConfig)
 _PCFG = POINTER(LhPisaConfig)
+_RCFG = POINTER(LhRotaryConfig)
+_DCFG = POINTER(LhDenseConfig)
 # name -> argument types (all return lh_status unless listed in _RESTYPES)
 SIGNATURES = {
     "lh_plan": [_CFG, POINTER(LhPlanInfo)],
@@ -85,13 +102,18 @@ SIGNATURES = {
     "lh_pisa_plan": [_PCFG, POINTER(LhPisaInfo)],
     "lh_pisa_pool_keys": [_PCFG, _P, _P, _P],
     "lh_pisa_select": [_PCFG, _P, _P, _P, _P, _P, _P, _P],
+    "lh_rotary": [_RCFG, _P, _P, _P, _P, _P, _P, _P],
+    "lh_mask_spans_bytes": [c_int64, c_int64],
+    "lh_mask_spans": [c_int64, c_int64, c_int32, _P, _P, _P, _P],
+    "lh_dense_fwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "lh_dense_bwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "lh_selftest_wait_timeout": [_P, c_size_t, c_int64, _P],
     "lh_check_error": [_P, _P],
     "lh_clear_error": [_P, _P],
     "lh_status_string": [c_int],
     "lh_last_error_message": [],
 }
-_RESTYPES = {"lh_status_string": c_char_p, "lh_last_error_message": c_char_p}
+_RESTYPES = {"lh_mask_spans_bytes": c_size_t, "lh_status_string": c_char_p, "lh_last_error_message": c_char_p}
 
 _lib = None
 

@@ -363,8 +363,9 @@ class LighthouseAttentionFn(torch.autograd.Function):
 
 
 def lighthouse_attention(q, k, v, L: int, p: int, k_budget: int, chunk: int = 2048, scorer: str = "qk_sum",
-                         selection: str = "parents"):
-    """One Lighthouse attention layer over causal q, k, v of shape [B, H, N, d]."""
+                         selection: str = "parents", rotary=None, positions=None):
+    """One Lighthouse attention layer over causal q, k, v of shape [B, H, N, d].  rotary (a dense.Rotary): positions
+    are applied to q and k before the pooling, as the dense attention applies them."""
     if q.dim() != 4:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [B, H, N, d]")
     B, H, N, d = q.shape
@@ -374,4 +375,7 @@ def lighthouse_attention(q, k, v, L: int, p: int, k_budget: int, chunk: int = 20
         _need(name, t, q.dtype, shape=q.shape)
     dtype = {torch.bfloat16: "bf16", torch.float32: "fp32"}[q.dtype]
     layer = Layer(B, H, N, d, L, p, k_budget, chunk, dtype, scorer, selection)
+    if rotary is not None:
+        from .dense import apply_rotary
+        q, k = apply_rotary(q, k, rotary, positions)
     return LighthouseAttentionFn.apply(q, k, v, layer)

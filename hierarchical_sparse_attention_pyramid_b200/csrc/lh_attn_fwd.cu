@@ -381,6 +381,24 @@ bool make_f32_map(CUtensorMap* m, const void* base, int64_t BH, int64_t rows, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [B][H][N][D] 16-bit tensor, {batch, head, token} strides in elements, viewed
+// as a 4-D tensor (D, N, H, B); box of 64 x 128 x 1 x 1, 128-byte swizzle.
+// The stride of a dimension of one is never used and need not be valid.
+bool make_head_map(CUtensorMap* m, const void* base, int dtype, int64_t B, int64_t H, int64_t N, int D,
+                   const int64_t* stride) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)(N > 1 ? stride[2] : D) * 2, (cuuint64_t)(H > 1 ? stride[1] : D) * 2,
+                           (cuuint64_t)(B > 1 ? stride[0] : D) * 2};
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, dtype == LH_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_attn_fwd(int64_t BH, int64_t S, int d, const void* qs, const void* ks, const void* vs, float* os,
                             float* lse, int* errw, cudaStream_t st, long long wait_cycles, int issue_loads, int64_t qt0,
                             int64_t qt1) {

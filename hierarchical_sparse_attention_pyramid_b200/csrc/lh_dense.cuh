@@ -1,0 +1,143 @@
+// Masked dense attention over all N tokens (forward and backward): what the
+// kernels share.
+//
+// Every mask here leaves each query i one interval of keys [lo_i, hi_i): its
+// document up to itself (causal), extended to the document's leading prefix
+// tokens; an empty interval for padding.  Seen from a key j the queries are
+// an interval too.  lh_mask_spans writes both, and for each tile of 128 rows
+// the least and the greatest bounds, from which a kernel takes the range of
+// tiles it visits and which of them need no masking.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "lh_common.cuh"
+#include "sm100.cuh"
+
+namespace lh {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// bounds of the non-empty rows of one 128-row tile
+struct TileSpan {
+  int min_lo, max_hi;  // union of the rows' intervals: [min_lo, max_hi); min_lo >= max_hi: every row is empty
+  int max_lo, min_hi;  // what every row sees: [max_lo, min_hi) (empty as soon as one row is)
+};
+
+struct MaskView {
+  const int2* rows;          // [B][N] keys of a query; NULL: computed from `causal`
+  const int2* cols;          // [B][N] queries of a key
+  const TileSpan* row_tile;  // [B][n_tiles]
+  const TileSpan* col_tile;  // [B][n_tiles]
+  int causal;
+};
+
+__device__ __forceinline__ int2 mask_row(const MaskView& m, int b, int i, int N) {
+  if (i >= N) return make_int2(0, 0);
+  if (m.rows) return __ldg(m.rows + (int64_t)b * N + i);
+  return make_int2(0, m.causal ? i + 1 : N);
+}
+__device__ __forceinline__ int2 mask_col(const MaskView& m, int b, int j, int N) {
+  if (j >= N) return make_int2(0, 0);
+  if (m.cols) return __ldg(m.cols + (int64_t)b * N + j);
+  return make_int2(m.causal ? j : 0, N);
+}
+__device__ __forceinline__ TileSpan mask_row_tile(const MaskView& m, int b, int t, int N) {
+  if (m.rows) {
+    const int4 v = __ldg(reinterpret_cast<const int4*>(m.row_tile) + (int64_t)b * ((N + 127) / 128) + t);
+    return {v.x, v.y, v.z, v.w};
+  }
+  if (!m.causal) return {0, N, 0, N};
+  return {0, min(N, t * 128 + 128), 0, t * 128 + 1};
+}
+__device__ __forceinline__ TileSpan mask_col_tile(const MaskView& m, int b, int t, int N) {
+  if (m.cols) {
+    const int4 v = __ldg(reinterpret_cast<const int4*>(m.col_tile) + (int64_t)b * ((N + 127) / 128) + t);
+    return {v.x, v.y, v.z, v.w};
+  }
+  if (!m.causal) return {0, N, 0, N};
+  return {t * 128, N, min(N, t * 128 + 128) - 1, N};
+}
+
+// the pieces of a spans buffer (lh_mask_spans_bytes)
+struct SpanBuffer {
+  int4 *row_tile, *col_tile;  // [B][n_tiles]
+  int2 *rows, *cols;          // [B][N]
+  int* plain_from;            // [B][N] scratch
+};
+inline SpanBuffer span_buffer(void* p, int64_t B, int64_t N) {
+  const int64_t tiles = B * ((N + 127) / 128);
+  SpanBuffer s;
+  s.row_tile = static_cast<int4*>(p);
+  s.col_tile = s.row_tile + tiles;
+  s.rows = reinterpret_cast<int2*>(s.col_tile + tiles);
+  s.cols = s.rows + B * N;
+  s.plain_from = reinterpret_cast<int*>(s.cols + B * N);
+  return s;
+}
+inline size_t span_bytes(int64_t B, int64_t N) {
+  return (size_t)(B * ((N + 127) / 128)) * 2 * sizeof(int4) + (size_t)(B * N) * (2 * sizeof(int2) + sizeof(int));
+}
+
+// strides of a [B][H][N][d] tensor in elements (d contiguous)
+struct Strides {
+  int64_t b, h, n;
+};
+
+struct DenseArgs {
+  int B, N, Hq, Hkv, n_tiles;
+  float scale;      // of the scores
+  float softcap;    // 0: none
+  const float* slopes;  // [Hq] or NULL
+  MaskView mask;
+  float* lse;       // [B][Hq][N]
+  float* delta;     // [B][Hq][N]
+  int* errw;
+};
+
+// ---------------------------------------------------------------------------
+// 16-bit element types
+// ---------------------------------------------------------------------------
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return F16 ? sm100::pack_f16x2(lo, hi) : sm100::pack_bf16x2(lo, hi);
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+template <bool F16>
+__host__ __device__ constexpr uint32_t idesc16(int M, int N, bool a_mn, bool b_mn) {
+  return F16 ? sm100::idesc_f16(M, N, a_mn, b_mn) : sm100::idesc_bf16(M, N, a_mn, b_mn);
+}
+
+// tanh from one exponential and one reciprocal: its absolute error (~1e-7) is
+// what matters, since the capped score is softcap * tanh
+__device__ __forceinline__ float tanh_abs(float y) {
+  float r;
+  const float e = sm100::fast_exp2(y * (2.f * kLog2e));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+  return fmaf(-2.f, r, 1.f);
+}
+
+// 4-D tensor map of a strided 16-bit tensor (with the sequence maps, lh_attn_fwd.cu)
+bool make_head_map(CUtensorMap* m, const void* base, int dtype, int64_t B, int64_t H, int64_t N, int D,
+                   const int64_t* stride);
+
+cudaError_t launch_mask_spans(const int32_t* docs, const uint8_t* prefix, int64_t B, int N, int causal,
+                              const SpanBuffer& s, cudaStream_t st);
+cudaError_t launch_dense_fwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
+                             const CUtensorMap& v, void* o, const Strides& so, cudaStream_t st);
+cudaError_t launch_dense_bwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
+                             const CUtensorMap& v, const CUtensorMap& go, const void* o, const Strides& so,
+                             const void* dout, const Strides& sdo, void* dq, const Strides& sdq, void* dk,
+                             const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st);
+
+}  // namespace lh

@@ -1,0 +1,336 @@
+"""torch front end of the dense attention around the layer (include/lh.h,
+lh_rotary, lh_mask_spans, lh_dense_fwd, lh_dense_bwd): rotary positions, masks
+over packed documents, and the masked attention with its gradient that a model
+trained with the Lighthouse layer resumes on.  Only marshalling: outputs are
+allocated with torch and every step runs in the library's kernels.
+
+Tensors are [B, H, N, d] with any batch, head and token strides that the
+kernels can address (channels contiguous; the attention: multiples of 8
+elements), so views of token-major projections need no copy.  The `*_forward`
+and `*_backward` calls and `rotary` refuse other tensors; `dense_attention` and
+`apply_rotary`, the autograd forms, copy them first.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from ._lib import LhDenseConfig, LhRotaryConfig
+
+_NAMES = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
+_err_words: dict = {}
+
+
+def _err(device) -> ctypes.c_void_p:
+    """The error word of a device: the calls below report into it (lh_check_error
+    clears it), see check_dense_error."""
+    t = _err_words.get(device.index)
+    if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            return None  # the first call on a device is a captured one: not reported
+        t = _err_words[device.index] = torch.zeros(_lib.ERR_WORD_BYTES, dtype=torch.uint8, device=device)
+        torch.cuda.current_stream(device).synchronize()
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def check_dense_error(device=None) -> None:
+    """Synchronise the current stream and raise if a dense attention, rotary or
+    cache call on this device reported a timeout or a bad index."""
+    device = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index or 0)
+    if device.index in _err_words:
+        _call("lh_check_error", device, _err(device))
+
+
+def _call(name: str, device, *args) -> None:
+    """A library call on a device's current stream (also when another device is current)."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if device.index == torch.cuda.current_device():
+        _lib.call(name, *args, stream)
+    else:
+        with torch.cuda.device(device):
+            _lib.call(name, *args, stream)
+
+
+def _ptr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _tensor(name: str, t, device=None, dtype=None, shape=None):
+    """Host check of an argument before its pointer reaches the library, which cannot see sizes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: liblh takes CUDA tensors")
+    return t
+
+
+def _flat(name: str, t, device, dtype, shape):
+    _tensor(name, t, device, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t
+
+
+def _addressable(t) -> bool:
+    """Rows of 16-byte units: what the attention kernels can load without a copy."""
+    return (t.stride(-1) == 1 and t.data_ptr() % 16 == 0
+            and all(n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])))
+
+
+def _strides(t):
+    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+# ------------------------------------------------------------------ rotary positions
+
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       original: int = 8192, fast_turns: float = 32.0, slow_turns: float = 1.0, device="cuda"):
+    """-> (frequencies [rot/2] float64, amplitude): radians a position of each rotated pair, base^(-2i/rot), for a
+    context stretched by `factor` over the `original` length with scaling
+    - "linear": positions divided by the factor;
+    - "ntk": the base raised to base * factor^(rot / (rot - 2)), which stretches the slowest pair by the factor and
+      leaves the fastest;
+    - "yarn": pairs that make more than fast_turns turns in the original length are left, those that make fewer than
+      slow_turns are divided by the factor, with a linear blend between; the amplitude is 0.1 ln(factor) + 1."""
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot: {rot}, expected an even number of channels")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling: {scaling!r}, expected None, 'linear', 'ntk' or 'yarn'")
+    if not base > 1 or not factor >= 1 or original < 1:
+        raise ValueError("expected base > 1, factor >= 1 and original >= 1")
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    i = torch.arange(0, rot, 2, dtype=torch.float64)
+    f = float(base) ** (-i / max(rot, 1))
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn" and factor > 1:
+        at = [rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+              for turns in (fast_turns, slow_turns)]
+        lo, hi = max(0, math.floor(at[0])), min(rot - 1, math.ceil(at[1]))
+        ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * (1 - ramp) + f / factor * ramp
+        amplitude = 0.1 * math.log(factor) + 1.0
+    return f.to(device), amplitude
+
+
+@dataclass(frozen=True)
+class Rotary:
+    """Rotary positions of a model: what `rotary` takes beside the tensors."""
+    frequencies: torch.Tensor  # [rot/2] float64
+    layout: str = "half"
+    amplitude: float = 1.0
+
+    @staticmethod
+    def make(rot: int, base: float = 10000.0, layout: str = "half", device="cuda", **scaling) -> "Rotary":
+        frequencies, amplitude = rotary_frequencies(rot, base, device=device, **scaling)
+        return Rotary(frequencies, layout, amplitude)
+
+
+def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: float = 1.0, inverse: bool = False,
+           out=None):
+    """Rotary positions of q [B, Hq, N, d] and k [B, Hk, N, d] (k None: q alone) -> (q', k').
+
+    The first 2 * len(frequencies) channels of each head are turned: pairs (i, i + rot/2) with layout "half",
+    (2i, 2i + 1) with "interleaved".  positions: int32 [B, N], or None for 0 .. N-1.  inverse turns back: the
+    gradient of a call is the inverse call on the output's gradient.  out: (q', k') to write, which may be (q, k)."""
+    _tensor("q", q)
+    if q.dim() != 4 or q.dtype not in _NAMES:
+        raise ValueError(f"q: shape {tuple(q.shape)} of {q.dtype}, expected [B, H, N, d] of bf16, fp16 or fp32")
+    B, Hq, N, d = q.shape
+    ts = [q] if k is None else [q, k]
+    if k is not None:
+        _tensor("k", k, q.device, q.dtype)
+        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
+            raise ValueError(f"k: shape {tuple(k.shape)}, expected ({B}, H, {N}, {d})")
+    if layout not in _lib.ROTARY_LAYOUTS:
+        raise ValueError(f"layout: {layout!r}, expected 'half' or 'interleaved'")
+    _tensor("frequencies", frequencies, q.device, torch.float64)
+    if frequencies.dim() != 1 or not frequencies.is_contiguous() or 2 * frequencies.numel() > d:
+        raise ValueError(f"frequencies: shape {tuple(frequencies.shape)}, expected at most {d // 2} in one row")
+    if positions is not None:
+        _flat("positions", positions, q.device, torch.int32, (B, N))
+    if out is None:
+        outs = [torch.empty_like(t) for t in ts]
+    else:
+        outs = list(out)[:len(ts)]
+        for name, o, t in zip(("out[0]", "out[1]"), outs, ts):
+            _tensor(name, o, q.device, q.dtype, t.shape)
+    for name, t in zip(("q", "k", "out[0]", "out[1]"), ts + outs):
+        if d > 1 and t.stride(-1) != 1 and t.numel():
+            raise ValueError(f"{name}: channels must be contiguous")
+    for name, o in zip(("out[0]", "out[1]"), outs):
+        if any(n > 1 and s == 0 for n, s in zip(o.shape, o.stride())):
+            raise ValueError(f"{name}: an expanded tensor cannot be written")
+    cfg = LhRotaryConfig(B, N, Hq, 0 if k is None else k.shape[1], d, 2 * frequencies.numel(),
+                         _lib.ROTARY_LAYOUTS[layout], _lib.DENSE_DTYPES[_NAMES[q.dtype]], int(inverse), amplitude,
+                         _strides(q), _strides(ts[-1]), _strides(outs[0]), _strides(outs[-1]))
+    if all(t.numel() for t in ts):
+        _call("lh_rotary", q.device, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(frequencies), _ptr(positions),
+              _ptr(outs[0]), _ptr(outs[1]) if k is not None else None)
+    return outs[0], (outs[1] if k is not None else None)
+
+
+class _RotaryFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, rope, positions):
+        ctx.rope, ctx.positions = rope, positions
+        q, k = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (q, k))
+        out = rotary(q, k, rope.frequencies, positions, rope.layout, rope.amplitude)
+        return out if k is not None else out[0]
+
+    @staticmethod
+    def backward(ctx, dq, dk=None):
+        rope = ctx.rope
+        dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
+        gq, gk = rotary(dq, dk, rope.frequencies, ctx.positions, rope.layout, rope.amplitude, inverse=True)
+        return gq, gk, None, None
+
+
+def apply_rotary(q, k, rope: Rotary, positions=None):
+    """`rotary` with its gradient.  k None: q alone (one tensor is returned)."""
+    return _RotaryFn.apply(q, k, rope, positions)
+
+
+# ------------------------------------------------------------------ masks
+
+@dataclass(frozen=True)
+class AttentionMask:
+    """A mask of the dense attention over B rows of N tokens; attention_mask makes it, every layer shares it."""
+    B: int
+    N: int
+    spans: torch.Tensor
+
+
+def attention_mask(docs=None, prefix=None, causal: bool = True) -> AttentionMask:
+    """The mask of packed rows.  docs: int32 [B, N], a document being a run of equal ids and a negative id padding
+    (None: a row is one document).  prefix: bool or uint8 [B, N]; the prefix tokens that lead a document are seen by
+    all of it.  causal: beyond that a token sees its document up to itself; otherwise all of it."""
+    some = docs if docs is not None else prefix
+    if some is None:
+        raise ValueError("attention_mask: docs or prefix needed (a plain causal mask needs none)")
+    _tensor("docs" if docs is not None else "prefix", some)
+    if some.dim() != 2 or some.numel() == 0:
+        raise ValueError(f"docs: shape {tuple(some.shape)}, expected a non-empty [B, N]")
+    B, N = some.shape
+    if docs is not None:
+        _flat("docs", docs, some.device, torch.int32, (B, N))
+    if prefix is not None:
+        if prefix.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"prefix: dtype {prefix.dtype}, expected bool or uint8")
+        _flat("prefix", prefix, some.device, prefix.dtype, (B, N))
+    spans = torch.empty(_lib.load().lh_mask_spans_bytes(B, N), dtype=torch.uint8, device=some.device)
+    _call("lh_mask_spans", some.device, ctypes.c_int64(B), ctypes.c_int64(N), ctypes.c_int32(bool(causal)), _ptr(docs),
+          _ptr(prefix), _ptr(spans))
+    return AttentionMask(B, N, spans)
+
+
+# ------------------------------------------------------------------ attention
+
+def _dense_config(q, k, v, mask, causal, scale, softcap, slopes):
+    _tensor("q", q)
+    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q: shape {tuple(q.shape)} of {q.dtype}, expected [B, H, N, d] of bf16 or fp16")
+    B, Hq, N, d = q.shape
+    _tensor("k", k, q.device, q.dtype)
+    if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d) or not k.shape[1] or Hq % k.shape[1]:
+        raise ValueError(f"k: shape {tuple(k.shape)}, expected ({B}, a divisor of {Hq}, {N}, {d})")
+    _tensor("v", v, q.device, q.dtype, k.shape)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not _addressable(t):
+            raise ValueError(f"{name}: strides {t.stride()}, expected contiguous channels in 16-byte rows")
+    if mask is not None:
+        if (mask.B, mask.N) != (B, N):
+            raise ValueError(f"mask: of {mask.B} x {mask.N} tokens, expected {B} x {N}")
+        if mask.spans.device != q.device:
+            raise ValueError(f"mask: on {mask.spans.device}, expected {q.device}")
+    if slopes is not None:
+        _flat("slopes", slopes, q.device, torch.float32, (Hq,))
+    return LhDenseConfig(B, N, Hq, k.shape[1], d, _lib.DENSE_DTYPES[_NAMES[q.dtype]], int(bool(causal)),
+                         1.0 / math.sqrt(d) if scale is None else scale, softcap, _strides(q), _strides(k),
+                         _strides(v))
+
+
+def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = True, scale: float | None = None,
+                  softcap: float = 0.0, slopes=None):
+    """Masked attention of q [B, Hq, N, d] over k, v [B, Hkv, N, d], bf16 or fp16 -> (o as q, lse [B, Hq, N] fp32).
+
+    mask: from attention_mask (causal is then the mask's); None: causal or full.  scale: 1/sqrt(d) unless given.
+    softcap > 0: scores x become softcap * tanh(x / softcap).  slopes: fp32 [Hq], scores get -slope |i - j|.
+    A query without keys gets o = 0, lse = -inf."""
+    cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
+    o = torch.empty_like(q)
+    if not _addressable(o):
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    cfg.o_stride = _strides(o)
+    _call("lh_dense_fwd", q.device, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v),
+          None if mask is None else _ptr(mask.spans), _ptr(slopes), _ptr(o), _ptr(lse), _err(q.device))
+    return o, lse
+
+
+def dense_backward(do, q, k, v, o, lse, mask: AttentionMask | None = None, causal: bool = True,
+                   scale: float | None = None, softcap: float = 0.0, slopes=None):
+    """Gradients of dense_forward's o with its inputs, o and lse -> (dq, dk, dv)."""
+    cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
+    for name, t in (("do", do), ("o", o)):
+        _tensor(name, t, q.device, q.dtype, q.shape)
+        if not _addressable(t):
+            raise ValueError(f"{name}: strides {t.stride()}, expected contiguous channels in 16-byte rows")
+    _flat("lse", lse, q.device, torch.float32, q.shape[:3])
+    grads = []
+    for n, t in (("dq", q), ("dk", k), ("dv", v)):
+        g = torch.empty_like(t)
+        if not _addressable(g):
+            g = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        grads.append(g)
+        setattr(cfg, n + "_stride", _strides(g))
+    cfg.o_stride, cfg.do_stride = _strides(o), _strides(do)
+    delta = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _call("lh_dense_bwd", q.device, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse),
+          None if mask is None else _ptr(mask.spans), _ptr(slopes), _ptr(delta), *(_ptr(g) for g in grads),
+          _err(q.device))
+    return tuple(grads)
+
+
+def _usable(t):
+    return t if _addressable(t) else t.contiguous()
+
+
+class _DenseAttentionFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, slopes, mask, opt):
+        q, k, v = _usable(q), _usable(k), _usable(v)
+        o, lse = dense_forward(q, k, v, mask, slopes=slopes, **opt)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.slopes, ctx.mask, ctx.opt = slopes, mask, opt
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse = ctx.saved_tensors
+        dq, dk, dv = dense_backward(_usable(do), q, k, v, o, lse, ctx.mask, slopes=ctx.slopes, **ctx.opt)
+        return dq, dk, dv, None, None, None
+
+
+def dense_attention(q, k, v, mask: AttentionMask | None = None, causal: bool = True, scale: float | None = None,
+                    softcap: float = 0.0, slopes=None, rotary: Rotary | None = None, positions=None):
+    """Masked attention with its gradient in q, k and v (arguments as dense_forward).  rotary: positions are applied
+    to q and k first."""
+    if slopes is not None and slopes.requires_grad:
+        raise ValueError("slopes: no gradient is computed for them")
+    if rotary is not None:
+        q, k = apply_rotary(q, k, rotary, positions)
+    return _DenseAttentionFn.apply(q, k, v, slopes, mask, dict(causal=causal, scale=scale, softcap=softcap))

@@ -55,7 +55,8 @@ typedef enum {
   LH_ERR_DEVICE = 6        /* a device-side index check failed (from lh_check_error) */
 } lh_status;
 
-typedef enum { LH_BF16 = 0, LH_FP32 = 1 } lh_dtype;
+/* LH_FP16: the dense attention, rotary and cache calls only (the layer takes bf16 or fp32) */
+typedef enum { LH_BF16 = 0, LH_FP32 = 1, LH_FP16 = 2 } lh_dtype;
 
 /* Level-0 score s0_t from the l2 norms of Q_t and K_t (LH-summary
  * "Technical details" (2): ||Q_i||_2, ||K_i||_2 are the scores at level 0). */
@@ -425,6 +426,95 @@ lh_status lh_pisa_pool_keys(const lh_pisa_config *cfg, const void *k, void *kpyr
  * level has fewer than topk candidates.  Level 0 is the selection. */
 lh_status lh_pisa_select(const lh_pisa_config *cfg, const void *q, const void *k, const void *kpyr,
                          int32_t *kept_idx, float *kept_score, void *ws, lh_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The dense attention around the layer.  Lighthouse pretraining ends in a
+ * resume with dense attention, and only the dense model can decode (LH-post
+ * "Limitations"; LH-summary "Method"): these calls are that attention as it is
+ * trained and served.  The pages fix nothing of it beyond softmax(Q K^T /
+ * sqrt(d)) V; the formulas are stated at each call.
+ *
+ * Unlike the layer's calls they take strides: every [B][H][N][d] tensor
+ * comes with {batch, head, token} strides in elements (channels contiguous),
+ * so tensors laid out tokens before heads need no copy.  `err` is the error
+ * word (LH_ERR_WORD_BYTES, as at the start of a ws; read by lh_check_error) or
+ * NULL, when device-side problems are not reported.  Calls keep no state and
+ * may be captured into graphs; calls that share an output or a scratch buffer
+ * must not overlap.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary positions.  Pair i of the first `rot` channels of each head is turned
+ * by angle a = position * freq[i] and scaled:
+ *   (x, y) -> amplitude (x cos a - y sin a, y cos a + x sin a),
+ * by -a with `inverse` (the adjoint, which turns gradients back).  Pair i is
+ * channels (i, i + rot/2) with LH_ROTARY_HALF and (2i, 2i + 1) with
+ * LH_ROTARY_INTERLEAVED.  Channels from rot on are copied.  The angle is
+ * reduced to a fraction of a turn in fp64. */
+typedef enum { LH_ROTARY_HALF = 0, LH_ROTARY_INTERLEAVED = 1 } lh_rotary_layout;
+
+typedef struct {
+  int64_t B, N;      /* batch, tokens */
+  int32_t Hq, Hk;    /* heads of q and of k (0: that tensor is absent) */
+  int32_t d, rot;    /* channels of a head; rotated channels: even, 0 <= rot <= d */
+  int32_t layout;    /* lh_rotary_layout */
+  int32_t dtype;     /* LH_BF16, LH_FP16 or LH_FP32 */
+  int32_t inverse;   /* 0 or 1 */
+  float amplitude;
+  int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+} lh_rotary_config;
+
+/* In: q, k; freq [rot/2] fp64, radians a position; positions [B][N] int32, or
+ * NULL for 0 .. N-1.  Out: q_out, k_out, which may be q, k themselves (with
+ * the same strides) and must not overlap them otherwise.  B = 0 or N = 0
+ * queues nothing. */
+lh_status lh_rotary(const lh_rotary_config *cfg, const void *q, const void *k, const double *freq,
+                    const int32_t *positions, void *q_out, void *k_out, lh_stream_t stream);
+
+/* Masks of the dense attention as spans.  A document is a run of equal ids in
+ * a row of docs [B][N] int32 (NULL: the whole row); tokens with a negative id
+ * are padding: they see nothing, nothing sees them, their outputs and
+ * gradients are 0.  prefix [B][N] (uint8, non-zero: a prefix token; NULL: none)
+ * counts for the tokens that lead their document, before its first plain
+ * token: the whole document sees those.  With causal a query sees its document
+ * up to itself and the prefix; without, the whole document.
+ * Out: spans (lh_mask_spans_bytes bytes, 16-byte aligned), read by
+ * lh_dense_fwd and lh_dense_bwd; every layer and both directions can share it. */
+size_t lh_mask_spans_bytes(int64_t B, int64_t N);
+lh_status lh_mask_spans(int64_t B, int64_t N, int32_t causal, const int32_t *docs, const uint8_t *prefix, void *spans,
+                        lh_stream_t stream);
+
+typedef struct {
+  int64_t B, N;      /* batch, tokens (queries and keys) */
+  int32_t Hq, Hkv;   /* query heads; key heads, a divisor: head h reads key head h / (Hq / Hkv) */
+  int32_t d;         /* 64 or 128 */
+  int32_t dtype;     /* LH_BF16 or LH_FP16 */
+  int32_t causal;    /* without spans: 1 = keys up to the query, 0 = all keys */
+  float scale;       /* of the scores, > 0 */
+  float softcap;     /* > 0: scores x become softcap * tanh(x / softcap); 0: not */
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+  int64_t do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3]; /* lh_dense_bwd only */
+} lh_dense_config;
+
+/* Masked attention: O_i = sum_j p_ij V_j, p_i the softmax over the keys j that
+ * the mask leaves query i of cap(scale Q_i . K_j) - slopes[h] |i - j|.
+ * In: q, k, v; spans from lh_mask_spans or NULL (see `causal`); slopes [Hq]
+ * fp32 (>= 0 for a penalty) or NULL.  Strides are multiples of 8 elements and
+ * pointers 16-byte aligned.
+ * Out: o; lse [B][Hq][N] fp32, the natural log of the row's sum of
+ * exponentials.  A query without keys has O = 0 and LSE = -inf.
+ * Probabilities enter P V rounded to the inputs' type; sums are fp32.  Values
+ * in padding and past N are not used; those of another document of the batch
+ * row must be finite. */
+lh_status lh_dense_fwd(const lh_dense_config *cfg, const void *q, const void *k, const void *v, const void *spans,
+                       const float *slopes, void *o, float *lse, void *err, lh_stream_t stream);
+
+/* Its gradients (none for the slopes), dK and dV summed over the query heads
+ * that share a key head; every gradient is written once, in an order that does
+ * not depend on scheduling.  In: the forward's inputs, o and lse, and dout.
+ * Scratch: delta [B][Hq][N] fp32 (left holding rowsum(dout * o)). */
+lh_status lh_dense_bwd(const lh_dense_config *cfg, const void *q, const void *k, const void *v, const void *o,
+                       const void *dout, const float *lse, const void *spans, const float *slopes, float *delta,
+                       void *dq, void *dk, void *dv, void *err, lh_stream_t stream);
 
 /* Self-test of the device-side timeout path (the pages have no counterpart).
  * Launches the stage-4 forward kernel on one 128-row tile (d = 64) with its
