@@ -20,6 +20,7 @@ STATUS_NAMES = {0: "LH_OK", 1: "LH_ERR_INVALID_ARG", 2: "LH_ERR_UNSUPPORTED", 3:
                 4: "LH_ERR_CUDA", 5: "LH_ERR_TIMEOUT", 6: "LH_ERR_DEVICE"}
 DTYPES = {"bf16": 0, "fp32": 1}
 DENSE_DTYPES = {"bf16": 0, "fp32": 1, "fp16": 2}  # the dense attention, rotary and cache calls
+CACHE_KINDS = {"bf16": 0, "fp16": 1, "e4m3": 2, "int8": 3}
 ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 SCORERS = {"qk_sum": 0, "k": 1, "q": 2}
 SELECTIONS = {"parents": 0, "direct": 1, "nested": 2}
@@ -71,11 +72,23 @@ class LhDenseConfig(ctypes.Structure):
                 + [(f"{n}_stride", c_int64 * 3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")])
 
 
+class LhCache(ctypes.Structure):
+    _fields_ = [("pages", c_int64), ("page", c_int32), ("heads", c_int32), ("d", c_int32), ("kind", c_int32),
+                ("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class LhCacheAttnConfig(ctypes.Structure):
+    _fields_ = [("seqs", c_int32), ("width", c_int32), ("Hq", c_int32), ("dtype", c_int32), ("max_tokens", c_int32),
+                ("n_tok", c_int64), ("scale", c_float), ("softcap", c_float), ("q_stride", c_int64 * 2)]
+
+
 _P = c_void_p
 _CFG = POINTER(LhConfig)
 _PCFG = POINTER(LhPisaConfig)
 _RCFG = POINTER(LhRotaryConfig)
 _DCFG = POINTER(LhDenseConfig)
+_CACHE = POINTER(LhCache)
+_ACFG = POINTER(LhCacheAttnConfig)
 # name -> argument types (all return lh_status unless listed in _RESTYPES)
 SIGNATURES = {
     "lh_plan": [_CFG, POINTER(LhPlanInfo)],
@@ -107,13 +120,17 @@ SIGNATURES = {
     "lh_mask_spans": [c_int64, c_int64, c_int32, _P, _P, _P, _P],
     "lh_dense_fwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "lh_dense_bwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "lh_cache_write": [_CACHE, c_int64, c_int32, _P, _P, _P, _P, _P, _P, _P],
+    "lh_cache_read": [_CACHE, c_int32, c_int32, _P, _P, c_int64, c_int32, _P, _P, _P, _P],
+    "lh_cache_attn_ws_bytes": [_CACHE, _ACFG],
+    "lh_cache_attn": [_CACHE, _ACFG, _P, _P, _P, _P, _P, _P, _P, _P, c_size_t, _P, _P],
     "lh_selftest_wait_timeout": [_P, c_size_t, c_int64, _P],
     "lh_check_error": [_P, _P],
     "lh_clear_error": [_P, _P],
     "lh_status_string": [c_int],
     "lh_last_error_message": [],
 }
-_RESTYPES = {"lh_mask_spans_bytes": c_size_t, "lh_status_string": c_char_p, "lh_last_error_message": c_char_p}
+_RESTYPES = {"lh_mask_spans_bytes": c_size_t, "lh_cache_attn_ws_bytes": c_size_t, "lh_status_string": c_char_p, "lh_last_error_message": c_char_p}
 
 _lib = None
 

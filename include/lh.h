@@ -430,7 +430,7 @@ lh_status lh_pisa_select(const lh_pisa_config *cfg, const void *q, const void *k
 /* ---------------------------------------------------------------------------
  * The dense attention around the layer.  Lighthouse pretraining ends in a
  * resume with dense attention, and only the dense model can decode (LH-post
- * "Limitations"; LH-summary "Method"): these calls are that attention as it is
+ * "Limitations and caveats"; LH-summary "Limitations"): these calls are that attention as it is
  * trained and served.  The pages fix nothing of it beyond softmax(Q K^T /
  * sqrt(d)) V; the formulas are stated at each call.
  *
@@ -515,6 +515,72 @@ lh_status lh_dense_fwd(const lh_dense_config *cfg, const void *q, const void *k,
 lh_status lh_dense_bwd(const lh_dense_config *cfg, const void *q, const void *k, const void *v, const void *o,
                        const void *dout, const float *lse, const void *spans, const float *slopes, float *delta,
                        void *dq, void *dk, void *dv, void *err, lh_stream_t stream);
+
+/* A paged key/value cache, as the dense attention is served.  k and v are
+ * [pages][heads][page][d] in the held type; the 8-bit kinds keep one fp32 scale
+ * per token and head, [pages][heads][page]: a row x is held as
+ * x * (top / max|x|), rounded to nearest even (top = 448 for e4m3, 127 for
+ * int8), with scale max|x| / top, and stands for held * scale.  A row with a
+ * NaN or an infinity stands for NaN. */
+typedef enum { LH_CACHE_BF16 = 0, LH_CACHE_FP16 = 1, LH_CACHE_E4M3 = 2, LH_CACHE_INT8 = 3 } lh_cache_kind;
+
+typedef struct {
+  int64_t pages;     /* pages of the cache */
+  int32_t page;      /* tokens of a page: a power of two, 8 .. 4096 */
+  int32_t heads, d;  /* key heads; channels of a head, 64 or 128 */
+  int32_t kind;      /* lh_cache_kind */
+  void *k, *v;
+  float *k_scale, *v_scale; /* 8-bit kinds, else NULL */
+} lh_cache;
+
+/* Write n tokens.  In: k, v [n][heads][d] of dtype (LH_BF16, LH_FP16 or
+ * LH_FP32) with {token, head} strides in elements; slots [n] int64: page id *
+ * page + row of each token, a negative one skipping its token.  A slot past
+ * the cache is skipped and sets the error word's bounds bit.  A slot may be
+ * given once in a call (which of two tokens stays is not defined). */
+lh_status lh_cache_write(const lh_cache *cache, int64_t n, int32_t dtype, const void *k, const void *v,
+                         const int64_t *k_stride, const int64_t *v_stride, const int64_t *slots, void *err,
+                         lh_stream_t stream);
+
+/* Read sequences back.  In: table [seqs][width] int32, the page of each
+ * page-sized run of a sequence's positions; starts [seqs + 1] int32: sequence
+ * s goes to rows starts[s] .. starts[s+1] - 1 of the outputs, its first
+ * positions.  Out: k_out, v_out [n][heads][d] of dtype, contiguous, 16-byte
+ * aligned; rows of no sequence are left as they are.  A page outside the cache
+ * leaves its rows as they are and sets the bounds bit. */
+lh_status lh_cache_read(const lh_cache *cache, int32_t seqs, int32_t width, const int32_t *table,
+                        const int32_t *starts, int64_t n, int32_t dtype, void *k_out, void *v_out, void *err,
+                        lh_stream_t stream);
+
+typedef struct {
+  int32_t seqs, width;   /* sequences; columns of the page table */
+  int32_t Hq;            /* query heads, a multiple of the cache's; at most 65535 / 16 sequences x row tiles */
+  int32_t dtype;         /* of q and o: LH_BF16 or LH_FP16; an unquantised cache holds the same type */
+  int32_t max_tokens;    /* most query tokens of one sequence (64 with a tree) */
+  int64_t n_tok;         /* query tokens of all sequences */
+  float scale, softcap;  /* as lh_dense_config */
+  int64_t q_stride[2];   /* token and head strides of q in elements */
+} lh_cache_attn_config;
+
+/* Attention of the newest tokens of each sequence over its cache.  Sequence
+ * s has lens[s] cached tokens, of which the last T_s are the query tokens
+ * q_start[s] .. q_start[s+1] - 1 (their keys and values are written before the
+ * call); q_start NULL: one query token a sequence.  Query token t sees the
+ * positions up to its own; with tree [n_tok] (uint64) it sees all positions
+ * before the T_s query tokens, and query token u of its sequence where bit u
+ * of its mask is set.  Formulas as lh_dense_fwd (slopes: distances between
+ * positions; not together with a tree).
+ * Out: o [n_tok][Hq][d] of dtype, contiguous; 0 where a token sees nothing;
+ * tokens of no sequence are left as they are.  ws: lh_cache_attn_ws_bytes
+ * bytes of scratch (its contents before and after do not matter; NULL when 0).
+ * Lengths and tables that do not fit (a page outside the cache, a length past
+ * the table, more than max_tokens tokens) are cut to what does and set the
+ * error word's bounds bit.  What the cache holds past a sequence's length is
+ * not used. */
+size_t lh_cache_attn_ws_bytes(const lh_cache *cache, const lh_cache_attn_config *cfg);
+lh_status lh_cache_attn(const lh_cache *cache, const lh_cache_attn_config *cfg, const void *q, const int32_t *table,
+                        const int32_t *lens, const int32_t *q_start, const uint64_t *tree, const float *slopes,
+                        void *o, void *ws, size_t ws_bytes, void *err, lh_stream_t stream);
 
 /* Self-test of the device-side timeout path (the pages have no counterpart).
  * Launches the stage-4 forward kernel on one 128-row tile (d = 64) with its
