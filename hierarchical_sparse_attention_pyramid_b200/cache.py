@@ -114,8 +114,8 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
     if cache.kind in ("bf16", "fp16") and cache.kind != _NAMES[q.dtype]:
         raise ValueError(f"q: {q.dtype}, expected the cache's {cache.k.dtype}")
     n, Hq, d = q.shape
-    if n and q.stride(-1) != 1:
-        raise ValueError("q: channels must be contiguous")
+    if n and (q.stride(-1) != 1 or q.data_ptr() % 16 or (n > 1 and q.stride(0) % 8) or (Hq > 1 and q.stride(1) % 8)):
+        raise ValueError(f"q: strides {q.stride()}, expected contiguous channels in 16-byte rows")
     _flat("lens", lens, cache.device, torch.int32, (seqs,))
     if q_start is not None:
         _flat("q_start", q_start, cache.device, torch.int32, (seqs + 1,))
@@ -131,7 +131,7 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
         _flat("out", out, q.device, q.dtype, q.shape)
     cfg = LhCacheAttnConfig(seqs, width, Hq, _lib.DENSE_DTYPES[_NAMES[q.dtype]], max_tokens, n,
                             1.0 / math.sqrt(d) if scale is None else scale, softcap,
-                            (ctypes.c_int64 * 2)(*q.stride()[:2]))
+                            (ctypes.c_int64 * 2)(q.stride(0), q.stride(1) if Hq > 1 else d))
     need = _lib.load().lh_cache_attn_ws_bytes(ctypes.byref(cache.c), ctypes.byref(cfg))
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     _call("lh_cache_attn", q.device, ctypes.byref(cache.c), ctypes.byref(cfg), _ptr(q), _ptr(page_table), _ptr(lens),

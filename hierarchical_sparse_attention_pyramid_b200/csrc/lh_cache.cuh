@@ -39,16 +39,16 @@ struct CacheAttnArgs {
   const float* slopes;          // [Hq] or NULL
   int seqs, width, Hq, max_tokens;
   float scale, softcap;
-  int splits, chunk;            // parts of a sequence's keys, and their size (set by the host)
-  float* part_o;                // [n_tok * Hq][splits][d]
-  float2* part_ml;              // [n_tok * Hq][splits] running maximum (log2 domain) and sum
+  int blocks;                   // of the grid, which share the work out (cache_attn_plan)
+  float* part_o;                // [blocks][2][row tile][d], NULL where no row can be in several blocks
+  float2* part_ml;              // [blocks][2][row tile] running maximum (log2 domain) and sum
   int* errw;
 };
 
 cudaError_t launch_cache_write(const CacheIoArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheIoArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int dtype, cudaStream_t st);
-// splits and chunk of a call (host only)
-void cache_attn_split(int64_t seqs, int64_t kv_heads, int64_t rows, int64_t longest, int* splits, int* chunk);
+// blocks of a call, and rows of its workspace (host only)
+void cache_attn_plan(int64_t seqs, int64_t kv_heads, int64_t rows, int64_t longest, int64_t* blocks, int64_t* places);
 
 }  // namespace lh

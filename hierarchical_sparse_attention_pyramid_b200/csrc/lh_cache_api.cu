@@ -25,7 +25,7 @@ lh_status check_cache(const lh_cache* c, const char* call, CacheView* v) {
   if (c->page < 8 || c->page > 4096 || (c->page & (c->page - 1)) != 0)
     return fail(LH_ERR_UNSUPPORTED, call, "page must be a power of two in [8, 4096]");
   if (c->kind < LH_CACHE_BF16 || c->kind > LH_CACHE_INT8) return fail(LH_ERR_INVALID_ARG, call, "bad kind");
-  if (c->pages > 0x7fffffffll || c->heads > 65535) return fail(LH_ERR_UNSUPPORTED, call, "too many pages or heads");
+  if (c->pages > 0x7fffffffll || c->heads > 65535 || c->pages * c->heads > 0xfffffffell / c->page) return fail(LH_ERR_UNSUPPORTED, call, "too many pages or heads");
   if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
     return fail(LH_ERR_INVALID_ARG, call, "k, v: NULL or not 16-byte aligned");
   const bool held8 = c->kind == LH_CACHE_E4M3 || c->kind == LH_CACHE_INT8;
@@ -53,19 +53,19 @@ lh_status check_attn(const lh_cache* c, const lh_cache_attn_config* g, const cha
   if (!(g->scale > 0.f) || !isfinite(g->scale)) return fail(LH_ERR_INVALID_ARG, call, "scale must be positive");
   if (!(g->softcap >= 0.f) || !isfinite(g->softcap))
     return fail(LH_ERR_INVALID_ARG, call, "softcap must be 0 or positive");
-  const int64_t tiles = ((int64_t)g->max_tokens * (g->Hq / c->heads) + 15) / 16;
-  if (g->Hq > 65535 || tiles > 65535 || tiles * g->seqs > 65535 || g->n_tok * g->Hq > 0x7fffffffll ||
+  if (g->Hq > 65535 || (int64_t)g->max_tokens * (g->Hq / c->heads) > (1 << 20) || g->n_tok > 0x7fffffffll / g->Hq ||
       (int64_t)g->width * c->page > ((int64_t)1 << 30))
     return fail(LH_ERR_UNSUPPORTED, call, "too many query tokens, sequences or positions");
   return LH_OK;
 }
 
-size_t attn_ws(const lh_cache* c, const lh_cache_attn_config* g, int* splits, int* chunk) {
-  *splits = *chunk = 0;
+// blocks, workspace rows and bytes of a call
+size_t attn_ws(const lh_cache* c, const lh_cache_attn_config* g, int64_t* blocks, int64_t* places) {
+  *blocks = *places = 0;
   if (g->seqs == 0 || g->n_tok == 0) return 0;
-  cache_attn_split(g->seqs, c->heads, (int64_t)g->max_tokens * (g->Hq / c->heads), (int64_t)g->width * c->page, splits,
-                   chunk);
-  return *splits == 1 ? 0 : (size_t)(g->n_tok * g->Hq) * *splits * (c->d * sizeof(float) + sizeof(float2));
+  cache_attn_plan(g->seqs, c->heads, (int64_t)g->max_tokens * (g->Hq / c->heads), (int64_t)g->width * c->page, blocks,
+                  places);
+  return (size_t)*places * (c->d * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
@@ -130,8 +130,8 @@ lh_status lh_cache_read(const lh_cache* cache, int32_t seqs, int32_t width, cons
 size_t lh_cache_attn_ws_bytes(const lh_cache* cache, const lh_cache_attn_config* cfg) {
   CacheView v;
   if (check_attn(cache, cfg, "lh_cache_attn_ws_bytes", &v) != LH_OK) return 0;
-  int splits, chunk;
-  return attn_ws(cache, cfg, &splits, &chunk);
+  int64_t blocks, places;
+  return attn_ws(cache, cfg, &blocks, &places);
 }
 
 lh_status lh_cache_attn(const lh_cache* cache, const lh_cache_attn_config* cfg, const void* q, const int32_t* table,
@@ -146,10 +146,13 @@ lh_status lh_cache_attn(const lh_cache* cache, const lh_cache_attn_config* cfg, 
   if (!q_start && (cfg->n_tok != cfg->seqs || cfg->max_tokens != 1))
     return fail(LH_ERR_INVALID_ARG, kCall, "without q_start there is one token a sequence");
   if (cfg->seqs == 0 || cfg->n_tok == 0) return LH_OK;
-  if (!q || !table || !lens || !o || !aligned(q, 2) || !aligned(o, 4) || !aligned(table, 4) || !aligned(lens, 4) ||
+  if (!q || !table || !lens || !o || !aligned(q, 16) || !aligned(o, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
       !aligned(q_start, 4) || !aligned(tree, 8) || !aligned(slopes, 4) || !aligned(err, 4))
     return fail(LH_ERR_INVALID_ARG, kCall, "NULL or misaligned pointer");
-  const size_t need = attn_ws(cache, cfg, &a.splits, &a.chunk);
+  if ((cfg->n_tok > 1 && cfg->q_stride[0] % 8 != 0) || cfg->q_stride[1] % 8 != 0)
+    return fail(LH_ERR_INVALID_ARG, kCall, "q_stride: strides must be multiples of 8 elements");
+  int64_t blocks, places;
+  const size_t need = attn_ws(cache, cfg, &blocks, &places);
   if (need && (!ws || !aligned(ws, 16))) return fail(LH_ERR_INVALID_ARG, kCall, "ws: NULL or not 16-byte aligned");
   if (ws_bytes < need) return fail(LH_ERR_WORKSPACE, kCall, "ws smaller than lh_cache_attn_ws_bytes");
   a.q = q;
@@ -168,8 +171,11 @@ lh_status lh_cache_attn(const lh_cache* cache, const lh_cache_attn_config* cfg, 
   a.max_tokens = cfg->max_tokens;
   a.scale = cfg->scale;
   a.softcap = cfg->softcap;
-  a.part_o = static_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (need ? (size_t)(cfg->n_tok * cfg->Hq) * a.splits * cache->d : 0));
+  a.blocks = (int)blocks;
+  if (need) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + places * cache->d);
+  }
   a.errw = static_cast<int*>(err);
   return done(launch_cache_attn(a, cfg->dtype, (cudaStream_t)stream), kCall);
 }

@@ -3,24 +3,33 @@
 //
 // Bound by reading the cache once: a key's row meets only the rows of its
 // head's group (tokens x Hq / Hkv), a few operations a byte.  So each warp
-// takes 16 keys at a time straight from global memory into registers, as the
-// operands of 16 x 8 x 16 matrix instructions, and no shared memory stands
-// between: K and V of the next 16 keys are asked for as soon as the registers
-// of the present ones are free, which keeps 4 to 8 KB a warp in flight.  The
-// order of the channels in Q K^T and of the output channels in P V is free, so
-// each lane loads 16 contiguous bytes of a row and calls them its fragment.
+// streams its keys through a ring of its own in shared memory (asynchronous
+// copies, 8 KB in flight a warp, no barrier between warps) and multiplies
+// them with matrix instructions of 16 keys (channels) x 8 query rows:
+// S^T = K Q^T and O^T = V^T P^T, so that 8 rows fill the instruction, which
+// is a group's size in decoding.  P^T turns from the layout of a result into
+// that of an operand by 8 x 8 transposes within the warp.  The order of the
+// channels in K Q^T and of the output channels in V^T P^T is free, so each
+// lane loads 16 contiguous bytes of a row and calls them its fragment.
 //
-// 8-bit values become 16-bit operands by moving bits: e4m3's exponent and
-// fraction are placed in a bf16 (fp16) as they are, which is the value times
-// 2^-120 (2^-8), exact also for subnormals, and undone in the score's scale
-// and the output's; int8 goes through the exact difference of two small
-// numbers.  The scale of a key enters its score, the scale of a value its
-// probability.
+// 8-bit values become fp16 operands, which hold them exactly: e4m3 by the
+// hardware's conversion, int8 as the difference of two fp16 numbers whose low
+// bits are the value's.  So that queries and probabilities are fp16 operands
+// too without leaving its range, a query row is multiplied by a power of two
+// that brings its largest value to 2^14 (exact; what is 2^28 times smaller
+// than that loses bits), and the probability times the value's scale is taken
+// relative to a power of two above the scales met so far.  The scale of a key
+// enters its score.
 //
-// One block of 4 warps takes one part of one sequence's keys for 16 query
-// rows of one head; the warps' running maxima, sums and outputs are joined in
-// shared memory in warp order, and the parts of a sequence by a second
-// kernel in part order, so that results do not depend on scheduling.
+// The work is a list of units of 128 keys: sequence by sequence, for each of
+// its heads and tiles of 8 to 32 query rows all the keys.  As many blocks of 4
+// warps as the GPU holds at once take equal stretches of that list, whatever
+// the lengths of the sequences are; a stretch may end inside one (sequence,
+// head, row tile) and begin inside another.  The warps' running maxima, sums
+// and outputs are joined in shared memory in warp order; what a block has of
+// an unfinished one goes to one of its two places in the workspace, and a
+// second kernel joins those in block order, so that results do not depend on
+// scheduling.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -32,12 +41,10 @@
 namespace lh {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kKeys = 16;  // keys of a warp's step
-// e4m3 as bf16 bits is the value times 2^-120: queries and probabilities are
-// raised by 2^60 so that products stay far from the subnormal range
-constexpr float kUp = 1152921504606846976.f;  // 2^60
+// query rows (tokens x heads of a group) that a block takes of `rows`
+int cache_attn_row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
+constexpr int kWarps = 4, kThreads = kWarps * 32;
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
@@ -54,388 +61,651 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// two held values, in bytes 1 and 3 of y (e4m3) or 0 and 2 (int8), as 16-bit
-// operands
-template <int KIND, bool F16>
-__device__ __forceinline__ uint32_t widen2(uint32_t y) {
+// two e4m3 bytes (the low half of y) as fp16
+__device__ __forceinline__ uint32_t e4m3_half2(uint32_t y) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(y));
+  return r;
+}
+// bytes i and j of y, int8 values raised by 128, as fp16: the bits of 1024 + u
+// less 1152
+__device__ __forceinline__ uint32_t u8_half2(uint32_t y, int i, int j) {
+  const uint32_t u = __byte_perm(y, 0x64646464u, (uint32_t)(i | 4 << 4 | j << 8 | 4 << 12));
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), off);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the four values of a word of one row: (0, 1), (2, 3)
+template <int KIND>
+__device__ __forceinline__ void widen_row(uint32_t w, uint32_t& b0, uint32_t& b1) {
   if constexpr (KIND == LH_CACHE_E4M3) {
-    if constexpr (F16) return (y & 0x80008000u) | ((y >> 1) & 0x3f803f80u);
-    return (y & 0x80008000u) | ((y >> 4) & 0x07f007f0u);
-  } else if constexpr (F16) {
-    // 1024 + (x + 128) as fp16 bits, less 1152
-    const uint32_t u = (y & 0x00ff00ffu) ^ 0x64806480u;
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&h);
+    b0 = e4m3_half2(w);
+    b1 = e4m3_half2(w >> 16);
   } else {
-    // (128 + low 7 bits) - (128, or 256 for a negative value) as bf16
-    const uint32_t u = (y & 0x007f007fu) | 0x43004300u, w = (y & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&w));
-    return *reinterpret_cast<const uint32_t*>(&h);
+    w ^= 0x80808080u;
+    b0 = u8_half2(w, 0, 1);
+    b1 = u8_half2(w, 2, 3);
   }
 }
-// bytes i and j (0-3: of x, 4-7: of z) where widen2 wants them
+// the four columns of a word of two rows: b[i] = (x_i, z_i)
 template <int KIND>
-__device__ __forceinline__ uint32_t place(uint32_t x, uint32_t z, int i, int j) {
-  return KIND == LH_CACHE_E4M3 ? __byte_perm(x, z, (uint32_t)(i << 4 | j << 12)) : __byte_perm(x, z, (uint32_t)(i | j << 8));
+__device__ __forceinline__ void widen_cols(uint32_t x, uint32_t z, uint32_t (&b)[4]) {
+  uint32_t lo = __byte_perm(x, z, 0x5140), hi = __byte_perm(x, z, 0x7362);
+  if constexpr (KIND == LH_CACHE_E4M3) {
+    b[0] = e4m3_half2(lo);
+    b[1] = e4m3_half2(lo >> 16);
+    b[2] = e4m3_half2(hi);
+    b[3] = e4m3_half2(hi >> 16);
+  } else {
+    lo ^= 0x80808080u;
+    hi ^= 0x80808080u;
+    b[0] = u8_half2(lo, 0, 1);
+    b[1] = u8_half2(lo, 2, 3);
+    b[2] = u8_half2(hi, 0, 1);
+    b[3] = u8_half2(hi, 2, 3);
+  }
 }
 
-struct Row {     // one of a thread's two query rows
-  int limit;     // keys below are seen (the last tokens: by `bits` with a tree)
-  uint64_t bits;
-  float slope2, at;  // distance bias: slope, position
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {  // zeros where not live
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int W>
+__device__ __forceinline__ void lds(uint32_t (&x)[W], uint32_t at) {
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at));
+}
+
+// transpose of an 8 x 8 matrix of 16-bit elements held by a warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// shapes of one (D, kind): what a warp's ring holds
+template <int D, int KIND, int NB>
+struct Shape {
+  static constexpr bool kHeld8 = KIND == LH_CACHE_E4M3 || KIND == LH_CACHE_INT8;
+  static constexpr int kBytes = kHeld8 ? 1 : 2;
+  static constexpr int kRow = D * kBytes;                 // bytes of a key's row
+  static constexpr int kKeys = kRow <= 128 ? 32 : 16;     // keys of a warp's step: 4 or 8 KB of K and V
+  static constexpr int kTile = kKeys * kRow;              // K or V of a step
+  static constexpr int kStage = 2 * kTile + (kHeld8 ? 2 * kKeys * 4 : 0);
+  static constexpr int kStages = kTile >= 4096 ? 2 : 4;   // 16 KB a warp
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr bool kQShared = NB > 2;                // query fragments in shared memory instead of registers
+  static constexpr int kQ = kQShared ? NB * (D / 16) * 256 : 0;
+  static constexpr int kOutRow = D + 4;                   // floats of a row of the warps' results
+  static constexpr int kOut = kWarps * NB * 8 * (kOutRow + 2) * 4;  // over the ring
+  static constexpr int kSmem = kQ + (kRing > kOut ? kRing : kOut);
 };
 
-template <typename U>
-__device__ __forceinline__ U load_nc(const void* p);
-template <>
-__device__ __forceinline__ uint4 load_nc<uint4>(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+constexpr int kUnit = kWarps * 32;  // keys of a unit of work
+// Units that a (sequence, head, row tile) counts before its keys, for what a
+// block spends to begin and end one (measured: about what two units of keys
+// cost); they come first and hold no keys.
+constexpr int kBegin = 2;
+
+// tokens of a sequence, cut to what the call allows (an error is reported
+// once, by `report`)
+struct Seq {
+  int tok0, T, len;
+};
+__device__ __forceinline__ Seq load_seq(const CacheAttnArgs& a, int s, bool report) {
+  Seq q{s, 1, __ldg(a.lens + s)};
+  if (a.q_start) {
+    q.tok0 = __ldg(a.q_start + s);
+    q.T = __ldg(a.q_start + s + 1) - q.tok0;
+  }
+  const int most = a.width << a.c.log2_page;
+  if (q.T < 0 || q.T > a.max_tokens || q.tok0 < 0 || q.tok0 + (int64_t)q.T > a.n_tok || q.len < 0 || q.len > most) {
+    if (report) report_error(a.errw, ERRW_BOUNDS);
+    q.T = max(0, min(q.T, a.max_tokens));
+    if (q.tok0 < 0 || q.tok0 + (int64_t)q.T > a.n_tok) q.T = 0;
+    q.len = max(0, min(q.len, most));
+  }
+  return q;
 }
-template <>
-__device__ __forceinline__ uint2 load_nc<uint2>(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ int key_units(int len) { return kBegin + max(1, (len + kUnit - 1) / kUnit); }
+// units of a sequence: heads x row tiles x units of each
+__device__ __forceinline__ int64_t seq_units(const CacheAttnArgs& a, const Seq& q, int rows_per_tile) {
+  const int tiles = (q.T * (a.Hq / a.c.heads) + rows_per_tile - 1) / rows_per_tile;
+  return (int64_t)a.c.heads * tiles * key_units(q.len);
+}
+// sum over the block of a value per thread (N warps); scratch: N + 1 int64
+template <int N>
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int64_t t = 0;
+#pragma unroll
+  for (int w = 0; w < N; ++w) t += scratch[w];
+  __syncthreads();
+  return t;
 }
 
-template <int D, int KIND, bool F16>
-__global__ void __launch_bounds__(kThreads, 3) cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
-  constexpr bool HELD8 = KIND == LH_CACHE_E4M3 || KIND == LH_CACHE_INT8;
-  constexpr int BYTES = HELD8 ? 1 : 2;
-  constexpr int E = 16 / BYTES;             // channels of a 16-byte load
-  constexpr int KC = D / (4 * E);           // K loads of a lane and key (4 lanes a key)
+// NB: tiles of 8 query rows that a block takes (each conversion of a held
+// value then serves NB matrix instructions)
+template <int D, int KIND, bool F16, int NB>
+__global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
+    cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
+  using Sh = Shape<D, KIND, NB>;
+  constexpr bool HELD8 = Sh::kHeld8, HALF = F16 || HELD8;  // HALF: fp16 matrix operands
+  constexpr int BYTES = Sh::kBytes, ROW = Sh::kRow, STAGES = Sh::kStages, KEYS = Sh::kKeys, NT = KEYS / 8;
+  constexpr int E = 16 / BYTES;             // channels of a 16-byte unit
   constexpr int STEPS = D / 16;             // matrix steps over the channels
-  constexpr int VB = D * BYTES / 8 < 16 ? D * BYTES / 8 : 16;  // bytes of a V load (8 lanes a key)
+  constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;  // bytes of a V load (8 lanes a key)
   constexpr int VE = VB / BYTES, VC = D / (8 * VE), VW = VB / 4;
-  constexpr bool PF16 = F16 && !HELD8;      // type of P and V: bf16 for 8-bit values, whose scales would push
-                                            // probabilities below fp16's range
-  constexpr float kDown = KIND == LH_CACHE_E4M3 ? (F16 ? 256.f : kUp) : 1.f;  // what a raw score is short of
-  constexpr float kPUp = KIND == LH_CACHE_E4M3 ? kUp : 1.f;
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint4* sQ = reinterpret_cast<uint4*>(smem);               // [STEPS][32] fragments of the 16 query rows
-  float* sO = reinterpret_cast<float*>(smem);               // later [kWarps][16][D]
-  float* sML = reinterpret_cast<float*>(smem + kWarps * 16 * D * 4);  // [kWarps][16][2]
+  constexpr float kPUp = HELD8 ? 64.f : 1.f;  // raises probabilities (at most 2^8) within fp16's range
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint2* sQ = reinterpret_cast<uint2*>(smem);                           // [NB][STEPS][32] where shared
+  float* sO = reinterpret_cast<float*>(smem + Sh::kQ);                  // later [kWarps][NB * 8][kOutRow]
+  float* sML = sO + kWarps * NB * 8 * Sh::kOutRow;                      // [kWarps][NB * 8][2]
+
+  __shared__ int64_t sScan[kWarps + 2];
+  __shared__ int sSeq;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int part = blockIdx.x, hk = blockIdx.y;
   const int G = a.Hq / a.c.heads;
-  const int row_tiles = (a.max_tokens * G + 15) / 16;
-  const int s = blockIdx.z / row_tiles, rt = blockIdx.z % row_tiles;
-  int tok0 = s, T = 1;
-  if (a.q_start) {
-    tok0 = __ldg(a.q_start + s);
-    T = __ldg(a.q_start + s + 1) - tok0;
-  }
-  if (T < 0 || T > a.max_tokens || tok0 < 0 || tok0 + (int64_t)T > a.n_tok) {
-    if (threadIdx.x == 0) report_error(a.errw, ERRW_BOUNDS);
-    T = max(0, min(T, a.max_tokens));
-    if (tok0 < 0 || tok0 + (int64_t)T > a.n_tok) return;
-  }
-  if (rt * 16 >= T * G) return;
-  int len = __ldg(a.lens + s);
-  if (len < 0 || (int64_t)len > (int64_t)a.width << a.c.log2_page) {
-    if (threadIdx.x == 0) report_error(a.errw, ERRW_BOUNDS);
-    len = max(0, min(len, a.width << a.c.log2_page));
-  }
-  const int64_t k_begin = (int64_t)part * a.chunk;
-  const int k0 = (int)(k_begin < len ? k_begin : len), k1 = min(len, k0 + a.chunk);
-  if (part > 0 && k0 >= len) return;  // the join knows how many parts a sequence has
-  const int ctx = len - T;            // keys before the query tokens' own
-
-  // ------------------------------------------------------------ Q fragments, the thread's rows
-  const int n_rows = T * G;
-  Row row[2];
+  // ------------------------------------------------------------ the block's stretch of the work
+  // a thread sums the units of a run of sequences; the one whose run holds the
+  // stretch's first unit looks for its sequence
+  int64_t u, u_end;
+  int s;
+  int64_t in_seq;  // u within its sequence
+  {
+    const int per = (a.seqs + kThreads - 1) / kThreads;
+    const int s0 = min(a.seqs, (int)threadIdx.x * per), s1 = min(a.seqs, s0 + per);
+    int64_t mine = 0;
+    for (int i = s0; i < s1; ++i) mine += seq_units(a, load_seq(a, i, blockIdx.x == 0), 8 * NB);
+    int64_t incl = mine;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = rt * 16 + g + x * 8;
-    const int tk = r < n_rows ? r / G : 0, h = hk * G + (r < n_rows ? r % G : 0);
-    row[x].limit = r < n_rows ? (a.tree ? ctx : ctx + tk + 1) : 0;
-    row[x].bits = a.tree && r < n_rows ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree) + tok0 + tk) : 0;
-    row[x].slope2 = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-    row[x].at = (float)(ctx + tk);
-  }
-  for (int i = threadIdx.x; i < STEPS * 32; i += kThreads) {
-    const int l = i & 31, st = i >> 5, gg = l >> 2, tt = l & 3;
-    const int c = st / (E / 4), j = st % (E / 4);
-    const int ch = c * 4 * E + tt * E + 4 * j;  // the lane's four channels of this step
-    uint32_t f[4];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = rt * 16 + gg + x * 8;
-      uint32_t w0 = 0, w1 = 0;
-      if (r < n_rows) {
-        const uint16_t* p = static_cast<const uint16_t*>(a.q) + (int64_t)(tok0 + r / G) * a.q_stride[0] +
-                            (int64_t)(hk * G + r % G) * a.q_stride[1] + ch;
-        w0 = p[0] | (uint32_t)p[1] << 16;
-        w1 = p[2] | (uint32_t)p[3] << 16;
-        if constexpr (KIND == LH_CACHE_E4M3 && !F16) {
-          const float2 u = unpack2<false>(w0), v = unpack2<false>(w1);
-          w0 = pack2<false>(u.x * kUp, u.y * kUp);
-          w1 = pack2<false>(v.x * kUp, v.y * kUp);
-        }
-      }
-      f[x] = w0;
-      f[2 + x] = w1;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
     }
-    sQ[i] = make_uint4(f[0], f[1], f[2], f[3]);
-  }
-  __syncthreads();
-
-  // ------------------------------------------------------------ keys
-  const int page_mask = (1 << a.c.log2_page) - 1;
-  // rows of a page are 16 keys or more apart from the next page, or 8: a
-  // tile of 8 keys lies in one page
-  auto page_of = [&](int key) -> int {  // key a multiple of 8
-    if (key >= k1) return -1;
-    const int p = __ldg(a.table + (int64_t)s * a.width + (key >> a.c.log2_page));
-    if (p < 0 || p >= a.c.pages) {
-      if (lane == 0) report_error(a.errw, ERRW_BOUNDS);
-      return -1;
-    }
-    return p;
-  };
-  // first row of the tile of 8 keys in the cache's rows, -1 without one
-  auto row_of = [&](int key, int page) -> int64_t {
-    return page < 0 ? -1 : (((int64_t)page * a.c.heads + hk) << a.c.log2_page) + (key & page_mask);
-  };
-  using KV16 = uint4;
-  using VLoad = typename std::conditional<VB == 16, uint4, uint2>::type;
-  uint32_t kr[2][KC][4];      // [tile of 8 keys][load]: key g of the tile
-  uint32_t vr[2][2][VC][VW];  // [tile][row 2t + x][load]
-  float ksc[2][2], vsc[2][2]; // scales of keys 2t, 2t+1 of each tile
-  int64_t rows[2];            // of the step whose K is loaded
-  auto load_k = [&](int key) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const bool live = rows[j] >= 0 && key + 8 * j + g < k1;
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        KV16 u = make_uint4(0, 0, 0, 0);
-        if (live) u = load_nc<uint4>(static_cast<const char*>(a.c.k) + ((rows[j] + g) * D + c * 4 * E + t * E) * BYTES);
-        kr[j][c][0] = u.x, kr[j][c][1] = u.y, kr[j][c][2] = u.z, kr[j][c][3] = u.w;
-      }
-      if constexpr (HELD8) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const bool lv = rows[j] >= 0 && key + 8 * j + 2 * t + x < k1;
-          ksc[j][x] = lv ? __ldg(a.c.k_scale + rows[j] + 2 * t + x) : 0.f;
-        }
-      }
-    }
-  };
-  auto load_v = [&](int key) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bool live = rows[j] >= 0 && key + 8 * j + 2 * t + x < k1;
-#pragma unroll
-        for (int c = 0; c < VC; ++c) {
-          VLoad u{};
-          if (live)
-            u = load_nc<VLoad>(static_cast<const char*>(a.c.v) +
-                               ((rows[j] + 2 * t + x) * D + c * 8 * VE + g * VE) * BYTES);
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&u);
-#pragma unroll
-          for (int i = 0; i < VW; ++i) vr[j][x][c][i] = w[i];
-        }
-        if constexpr (HELD8) vsc[j][x] = live ? __ldg(a.c.v_scale + rows[j] + 2 * t + x) : 0.f;
-      }
-  };
-
-  float acc[VC * VE][4];
-#pragma unroll
-  for (int i = 0; i < VC * VE; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  const bool cap = a.softcap > 0.f;
-  const float pre = (cap ? a.scale / a.softcap : a.scale * kLog2e) * kDown, cap2 = a.softcap * kLog2e;
-
-  int key = k0 + warp * kKeys;
-  int pg[2] = {page_of(key), page_of(key + 8)};
-  rows[0] = row_of(key, pg[0]);
-  rows[1] = row_of(key + 8, pg[1]);
-  load_k(key);
-  load_v(key);
-  for (; key < k1; key += kWarps * kKeys) {
-    const int next = key + kWarps * kKeys;
-    const bool bad[2] = {rows[0] < 0, rows[1] < 0};
-    rows[0] = row_of(next, page_of(next));
-    rows[1] = row_of(next + 8, page_of(next + 8));
-    // S of the 16 rows and 16 keys
-    float sc[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
-#pragma unroll
-    for (int st = 0; st < STEPS; ++st) {
-      const uint4 q4 = sQ[st * 32 + lane];
-      const uint32_t qa[4] = {q4.x, q4.y, q4.z, q4.w};
-      const int c = st / (E / 4), i = st % (E / 4);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t b0, b1;
-        if constexpr (HELD8) {
-          b0 = widen2<KIND, F16>(place<KIND>(kr[j][c][i], 0, 0, 1));
-          b1 = widen2<KIND, F16>(place<KIND>(kr[j][c][i], 0, 2, 3));
-        } else {
-          b0 = kr[j][c][2 * i];
-          b1 = kr[j][c][2 * i + 1];
-        }
-        mma<F16>(sc[j], qa, b0, b1);
-      }
-    }
-    float kf[2][2];
-    if constexpr (HELD8) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) kf[j][0] = ksc[j][0] * pre, kf[j][1] = ksc[j][1] * pre;
-    } else {
-      kf[0][0] = kf[0][1] = kf[1][0] = kf[1][1] = pre;
-    }
-    load_k(next);
-    // exponents of 2, masked
-    const bool edge = key + kKeys > (a.tree ? ctx : ctx + 1) || bad[0] || bad[1];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = e >> 1, kk = key + 8 * j + 2 * t + (e & 1);
-        float y = sc[j][e] * kf[j][e & 1];
-        if (cap) y = cap2 * tanh_abs(y);
-        if (a.slopes) y = fmaf(-row[x].slope2, fabsf(row[x].at - (float)kk), y);
-        if (edge) {
-          bool seen = kk < row[x].limit;
-          if (a.tree && kk >= ctx) seen = kk < len && ((row[x].bits >> (kk - ctx)) & 1);
-          if (!seen || bad[j] || kk >= k1) y = -INFINITY;
-        }
-        sc[j][e] = y;
-      }
-    uint32_t pa[4];
-    float alpha[2];
-    bool move = false;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float mx = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the reference moves only when the maximum exceeds it by more than 8
-      const bool mv = mx > m[x] + 8.f;
-      const float mn = mv ? mx : m[x];
-      alpha[x] = mv ? sm100::fast_exp2(m[x] - mn) : 1.f;
-      move |= mv;
-      m[x] = mn;
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      float p[2][2], sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          p[j][e] = sm100::fast_exp2(sc[j][2 * x + e] - ref);
-          sum += p[j][e];
-        }
-      l[x] = l[x] * alpha[x] + sum;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if constexpr (HELD8)
-          pa[2 * j + x] = pack2<PF16>(p[j][0] * (vsc[j][0] * kPUp), p[j][1] * (vsc[j][1] * kPUp));
-        else
-          pa[2 * j + x] = pack2<PF16>(p[j][0], p[j][1]);
-      }
-    }
-    if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-      for (int i = 0; i < VC * VE; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] *= alpha[e >> 1];
-    }
-#pragma unroll
-    for (int c = 0; c < VC; ++c)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        uint32_t b[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if constexpr (HELD8)
-            b[j] = widen2<KIND, PF16>(place<KIND>(vr[j][0][c][i / 4], vr[j][1][c][i / 4], i % 4, 4 + i % 4));
-          else
-            b[j] = __byte_perm(vr[j][0][c][i / 2], vr[j][1][c][i / 2], i % 2 ? 0x7632 : 0x5410);
-        }
-        mma<PF16>(acc[c * VE + i], pa, b[0], b[1]);
-      }
-    load_v(next);
-  }
-
-  // ------------------------------------------------------------ the warps' results
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-  }
-  __syncthreads();  // sQ's space is reused
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    if (t == 0) {
-      sML[(warp * 16 + g + x * 8) * 2] = m[x];
-      sML[(warp * 16 + g + x * 8) * 2 + 1] = l[x];
-    }
-  // accumulator i, element e: row g + 8 (e / 2), column 2t + e % 2 of the
-  // step, which is channel c * 8 VE + column * VE + i % VE
-#pragma unroll
-  for (int i = 0; i < VC * VE; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int ch = (i / VE) * 8 * VE + (2 * t + (e & 1)) * VE + i % VE;
-      sO[(warp * 16 + g + (e >> 1) * 8) * D + ch] = acc[i][e];
-    }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * D / 2; i += kThreads) {
-    const int r = i / (D / 2), ch = i % (D / 2) * 2;
-    const int rr = rt * 16 + r;
-    if (rr >= n_rows) continue;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sML[(w * 16 + r) * 2]);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float sum = 0.f, o0 = 0.f, o1 = 0.f;
+    if (lane == 31) sScan[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = sm100::fast_exp2(sML[(w * 16 + r) * 2] - ref);
-      const float2 u = *reinterpret_cast<const float2*>(sO + (w * 16 + r) * D + ch);
-      sum = fmaf(f, sML[(w * 16 + r) * 2 + 1], sum);
-      o0 = fmaf(f, u.x, o0);
-      o1 = fmaf(f, u.y, o1);
+      if (w < warp) before += sScan[w];
+      total += sScan[w];
     }
-    constexpr float kBack = KIND == LH_CACHE_E4M3 ? kUp : 1.f;  // the values' other 2^60
-    o0 *= kBack;
-    o1 *= kBack;
-    const int64_t out = (int64_t)(tok0 + rr / G) * a.Hq + hk * G + rr % G;
-    if (a.splits == 1) {
-      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      reinterpret_cast<uint32_t*>(a.o)[(out * D + ch) / 2] = pack2<F16>(o0 * inv, o1 * inv);
-    } else {
-      *reinterpret_cast<float2*>(a.part_o + (out * a.splits + part) * D + ch) = make_float2(o0, o1);
-      if (ch == 0) a.part_ml[out * a.splits + part] = make_float2(mm, sum);
+    before += incl - mine;
+    const int64_t blocks = min((int64_t)gridDim.x, total);  // no block has an empty stretch
+    if (blockIdx.x >= blocks) return;
+    u = total * blockIdx.x / blocks;
+    u_end = total * (blockIdx.x + 1) / blocks;
+    __syncthreads();
+    if (u >= before && u < before + mine) {
+      int i = s0;
+      int64_t at = u - before;
+      for (;;) {
+        const int64_t n = seq_units(a, load_seq(a, i, false), 8 * NB);
+        if (at < n) break;
+        at -= n;
+        ++i;
+      }
+      sSeq = i;
+      sScan[0] = at;
     }
+    __syncthreads();
+    s = sSeq;
+    in_seq = sScan[0];
+  }
+  Seq seq = load_seq(a, s, false);
+
+  while (u < u_end) {
+    // ------------------------------------------------------------ one (sequence, head, row tile), all or some of its keys
+    const int kt_n = key_units(seq.len);
+    const int row_tiles = (seq.T * G + 8 * NB - 1) / (8 * NB);
+    if (in_seq >= (int64_t)a.c.heads * row_tiles * kt_n) {  // the next sequence with units
+      in_seq = 0;
+      seq = load_seq(a, ++s, false);
+      continue;
+    }
+    const int inst = (int)(in_seq / kt_n), from = (int)(in_seq % kt_n);
+    const int to = (int)min((int64_t)kt_n, from + (u_end - u));
+    u += to - from;
+    in_seq += to - from;
+    if (to <= kBegin) continue;  // no keys
+    const int kt0 = max(from - kBegin, 0), kt1 = to - kBegin;
+    const int hk = inst / row_tiles, rt = inst % row_tiles;
+    const int tok0 = seq.tok0, len = seq.len;
+    const int r0 = rt * 8 * NB, n_rows = seq.T * G;  // row r: token r / G, head r % G of the group
+    const int k0 = kt0 * kUnit, k1 = min(len, kt1 * kUnit);
+    const int ctx = len - seq.T;        // keys before the query tokens' own
+
+    // ------------------------------------------------------------ the ring of keys
+    const int page_mask = (1 << a.c.log2_page) - 1;
+    const int32_t* table = a.table + (int64_t)s * a.width;
+    constexpr uint32_t kNone = 0xffffffffu;
+    // lane j looks up the 8 keys from key + 8 j on (pages hold 8 tokens or
+    // more): their first row among the cache's rows, kNone for none
+    auto look_up = [&](int key) -> uint32_t {
+      const int kk = key + 8 * lane;
+      if (lane >= NT || kk >= k1) return kNone;
+      const int p = __ldg(table + (kk >> a.c.log2_page));
+      if (p >= 0 && p < a.c.pages) return (((uint32_t)p * a.c.heads + hk) << a.c.log2_page) + (kk & page_mask);
+      report_error(a.errw, ERRW_BOUNDS);
+      return kNone;
+    };
+    const uint32_t ring = sm100::smem_u32(sO) + warp * (STAGES * Sh::kStage);
+    // 16-byte units of a row are permuted by the row, so that the lanes of one
+    // fragment load meet different banks: 4 lanes x 2 rows of K, 2 units x 4
+    // even (odd) rows of V
+    auto swz = [](int row, int unit) -> uint32_t {
+      constexpr int U = ROW / 16;
+      const int f = U >= 8 ? (((row >> 1) & 3) << 1) ^ ((row & 1) << 2) : (row >> 1) & 3;
+      return (uint32_t)(row * ROW + ((unit ^ f) << 4));
+    };
+    constexpr int U = ROW / 16, PER = KEYS * U / 32, RPI = 32 / U;  // copies a lane makes, rows of one round of copies
+    const char* k_lane = static_cast<const char*>(a.c.k) + (lane / U % 8) * ROW + (lane % U) * 16;
+    const char* v_lane = static_cast<const char*>(a.c.v) + (lane / U % 8) * ROW + (lane % U) * 16;
+    auto fetch = [&](int key, uint32_t rows, uint32_t base, auto whole) {
+      constexpr bool WHOLE = decltype(whole)::value;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const uint32_t r = __shfl_sync(0xffffffffu, rows, j);
+        const char* kp = k_lane + (uint64_t)(WHOLE || r != kNone ? r : 0u) * ROW;
+        const char* vp = v_lane + (uint64_t)(WHOLE || r != kNone ? r : 0u) * ROW;
+#pragma unroll
+        for (int i = 0; i < PER / NT; ++i) {
+          const int row = j * 8 + i * RPI + lane / U;
+          const bool live = WHOLE || (r != kNone && key + row < k1);
+          const uint32_t dst = base + swz(row, lane % U);
+          cp_async16(dst, live ? kp + i * RPI * ROW : kp, live);
+          cp_async16(dst + Sh::kTile, live ? vp + i * RPI * ROW : vp, live);
+        }
+      }
+      if constexpr (HELD8) {
+        const uint32_t r = __shfl_sync(0xffffffffu, rows, lane >> 3 & (NT - 1));
+        const bool live = lane < KEYS && (WHOLE || (r != kNone && key + lane < k1));
+        const uint64_t at = live ? (uint64_t)r + (lane & 7) : 0;
+        if (lane < KEYS) {
+          cp_async4(base + 2 * Sh::kTile + lane * 4, a.c.k_scale + at, live);
+          cp_async4(base + 2 * Sh::kTile + KEYS * 4 + lane * 4, a.c.v_scale + at, live);
+        }
+      }
+    };
+    constexpr int kStride = kWarps * KEYS;
+    int key = k0 + warp * KEYS, ahead = key;
+    unsigned bad = 0;  // bit NT * slot + j: 8 keys of a slot whose page is missing
+    uint32_t rows = look_up(ahead);
+    auto fetch_next = [&](int slot) {
+      if (ahead < k1) {
+        const uint32_t base = ring + slot * Sh::kStage;
+        const unsigned none = __ballot_sync(0xffffffffu, rows == kNone) & ((1u << NT) - 1);
+        if (none == 0 && ahead + KEYS <= k1) fetch(ahead, rows, base, std::true_type{});
+        else fetch(ahead, rows, base, std::false_type{});
+        bad = (bad & ~(((1u << NT) - 1) << (NT * slot))) | none << (NT * slot);
+        ahead += kStride;
+        rows = look_up(ahead);
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch_next(i);
+
+    // ------------------------------------------------------------ query rows
+    // Fragment of tile nb, step st: channels ch .. ch + 3 of row nb * 8 + g,
+    // ch = c * 4 E + t * E + 4 i with st = c * (E / 4) + i: of a 16-byte unit's
+    // channels (8 or 16) the lane's next four.  up: power of two that brings a
+    // bf16 row's largest value to [2^14, 2^15) for 8-bit keys
+    auto load_q = [&](int nb, uint2 (&f)[STEPS], float& up) {
+      const int r = r0 + nb * 8 + g;
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + (int64_t)(tok0 + r / G) * a.q_stride[0] +
+                          (int64_t)(hk * G + r % G) * a.q_stride[1] + t * E;
+#pragma unroll
+      for (int c = 0; c < D / (4 * E); ++c)
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (r < n_rows) u = __ldg(reinterpret_cast<const uint4*>(p + c * 4 * E + i * 8));
+          f[c * (E / 4) + 2 * i] = make_uint2(u.x, u.y);
+          f[c * (E / 4) + 2 * i + 1] = make_uint2(u.z, u.w);
+        }
+      up = 1.f;
+      if constexpr (HELD8 && !F16) {
+        unsigned top = 0;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+          top = max(max(top, max(f[i].x & 0x7fffu, f[i].x >> 16 & 0x7fffu)), max(f[i].y & 0x7fffu, f[i].y >> 16 & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top >>= 7;  // biased exponent
+        up = __uint_as_float(max(1u, min(254u, 268u - min(268u, top))) << 23);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const float2 x = unpack2<false>(f[i].x), y = unpack2<false>(f[i].y);
+          f[i] = make_uint2(pack2<true>(x.x * up, x.y * up), pack2<true>(y.x * up, y.y * up));
+        }
+      }
+    };
+    const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
+    const float pre = cap ? a.scale / a.softcap : a.scale * kLog2e, cap2 = a.softcap * kLog2e;
+    // this thread's columns of a tile: query rows nb * 8 + 2t, 2t + 1
+    float qf[NB][2];  // factor of the row's scores
+    uint2 qr[Sh::kQShared ? 1 : NB][STEPS];
+    static_assert(NB <= kWarps, "a warp a tile");
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float up;
+      if constexpr (Sh::kQShared) {
+        uint2 f[STEPS];
+        load_q(nb, f, up);  // every warp needs the factors; one of them leaves the fragments
+        if (warp == nb) {
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) sQ[(nb * STEPS + i) * 32 + lane] = f[i];
+        }
+      } else {
+        load_q(nb, qr[nb], up);
+      }
+      qf[nb][0] = pre / __shfl_sync(0xffffffffu, up, 8 * t);
+      qf[nb][1] = pre / __shfl_sync(0xffffffffu, up, 8 * t + 4);
+    }
+    if constexpr (Sh::kQShared) __syncthreads();
+
+    constexpr int MI = VC * VE / 2;  // accumulators of a tile: 16 output channels each
+    float acc[NB][MI][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nb][i][e] = 0.f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
+    float v_ref = 7.888609052210118e-31f;  // (2^-100) 8 bits: power of two at or above the value scales so far, which
+                                           // acc is relative to
+    const uint32_t k_at = swz(g, t), v_at0 = swz(2 * t, g * VB >> 4) + (g * VB & 15),
+                   v_at1 = swz(2 * t + 1, g * VB >> 4) + (g * VB & 15);
+
+    for (int slot = 0; key < k1; key += kStride, slot = slot + 1 == STAGES ? 0 : slot + 1) {
+      cp_wait<STAGES - 2>();
+      __syncwarp();  // every lane's copies of this step have landed, and its reads of the last one are done
+      fetch_next(slot == 0 ? STAGES - 1 : slot - 1);
+      const uint32_t base = ring + slot * Sh::kStage;
+      const unsigned missing = bad >> (NT * slot) & ((1u << NT) - 1);
+      // S^T: sc[nb][k2][e]: key 16 k2 + g + 8 (e / 2), row nb * 8 + 2t + e % 2
+      float sc[NB][NT / 2][4], s2[NB == 1 ? NT / 2 : 1][4];  // one row tile: even and odd steps apart (two chains)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int k2 = 0; k2 < NT / 2; ++k2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[nb][k2][e] = 0.f;
+            if constexpr (NB == 1) s2[k2][e] = 0.f;
+          }
+#pragma unroll
+      for (int c = 0; c < D / (4 * E); ++c) {
+        uint32_t kr[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) lds<4>(kr[j], base + (k_at ^ (uint32_t)(c << 6)) + j * 8 * ROW);
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          const int st = c * (E / 4) + i;
+#pragma unroll
+          for (int k2 = 0; k2 < NT / 2; ++k2) {
+            uint32_t ka[4];
+            if constexpr (HELD8) {
+              widen_row<KIND>(kr[2 * k2][i], ka[0], ka[2]);
+              widen_row<KIND>(kr[2 * k2 + 1][i], ka[1], ka[3]);
+            } else {
+              ka[0] = kr[2 * k2][2 * i];
+              ka[2] = kr[2 * k2][2 * i + 1];
+              ka[1] = kr[2 * k2 + 1][2 * i];
+              ka[3] = kr[2 * k2 + 1][2 * i + 1];
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const uint2 qb = Sh::kQShared ? sQ[(nb * STEPS + st) * 32 + lane] : qr[Sh::kQShared ? 0 : nb][st];
+              mma<HALF>(NB == 1 && (st & 1) ? s2[NB == 1 ? k2 : 0] : sc[nb][k2], ka, qb.x, qb.y);
+            }
+          }
+        }
+      }
+      if constexpr (NB == 1) {
+#pragma unroll
+        for (int k2 = 0; k2 < NT / 2; ++k2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[0][k2][e] += s2[k2][e];
+      }
+      float kf[NT], vf[NT];  // scales of key 8 j + g
+      if constexpr (HELD8) {
+        float v_new = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kf[j]) : "r"(base + 2 * Sh::kTile + (8 * j + g) * 4));
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vf[j]) : "r"(base + 2 * Sh::kTile + KEYS * 4 + (8 * j + g) * 4));
+          v_new = fmaxf(v_new, vf[j]);
+        }
+        if (__any_sync(0xffffffffu, v_new > v_ref)) {
+          const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(v_new));
+          const float up = __uint_as_float(max(27u, min(227u, (top + 0x7fffffu) >> 23)) << 23);
+          const float f = v_ref / up;
+          v_ref = up;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nb][i][e] *= f;
+        }
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(v_ref)) * kPUp;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) vf[j] *= inv;
+      }
+      // exponents of 2, masked; then the probabilities
+      const bool edge = key + KEYS > (a.tree ? ctx : ctx + 1) || missing;
+      uint32_t pb[NB][NT];  // P^T as operands
+      bool move = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) sc[nb][j / 2][2 * (j & 1) + x] *= HELD8 ? kf[j] * qf[nb][x] : qf[nb][x];
+        if (cap) {
+#pragma unroll
+          for (int k2 = 0; k2 < NT / 2; ++k2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nb][k2][e] = cap2 * tanh_abs(sc[nb][k2][e]);
+        }
+        if (bias) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = min(r0 + nb * 8 + 2 * t + x, n_rows - 1);
+            const float slope2 = __ldg(a.slopes + hk * G + r % G) * kLog2e, at = (float)(ctx + r / G);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              float& y = sc[nb][j / 2][2 * (j & 1) + x];
+              y = fmaf(-slope2, fabsf(at - (float)(key + 8 * j + g)), y);
+            }
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = r0 + nb * 8 + 2 * t + x;
+            const int limit = r < n_rows ? (a.tree ? ctx : ctx + r / G + 1) : 0;  // keys below are seen
+            uint64_t bits = 0;
+            if (a.tree && r < n_rows) bits = __ldg(reinterpret_cast<const unsigned long long*>(a.tree) + tok0 + r / G);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const int kk = key + 8 * j + g;
+              bool seen = kk < limit;
+              if (a.tree && kk >= ctx) seen = (bits >> (kk - ctx)) & 1;
+              if (!seen || kk >= k1 || (missing >> j) & 1) sc[nb][j / 2][2 * (j & 1) + x] = -INFINITY;
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k2 = 0; k2 < NT / 2; ++k2) mx = sm100::max3f(mx, sc[nb][k2][x], sc[nb][k2][2 + x]);
+          move |= mx > m[nb][x] + 8.f;
+        }
+      }
+      // The reference of the exponents moves only when some key exceeds it by
+      // more than 8 (so P stays <= 2^8), which most steps settle by one vote.
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float alpha[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = m[nb][x];
+#pragma unroll
+            for (int k2 = 0; k2 < NT / 2; ++k2) mx = sm100::max3f(mx, sc[nb][k2][x], sc[nb][k2][2 + x]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            alpha[x] = mx > m[nb][x] ? sm100::fast_exp2(m[nb][x] - mx) : 1.f;
+            m[nb][x] = mx;
+            l[nb][x] *= alpha[x];
+          }
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nb][i][e] *= alpha[e & 1];
+        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float ref0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], ref1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float p0 = sm100::fast_exp2(sc[nb][j / 2][2 * (j & 1)] - ref0);
+          const float p1 = sm100::fast_exp2(sc[nb][j / 2][2 * (j & 1) + 1] - ref1);
+          l[nb][0] += p0;
+          l[nb][1] += p1;
+          pb[nb][j] = transpose8(HELD8 ? pack2<true>(p0 * vf[j], p1 * vf[j]) : pack2<HALF>(p0, p1));
+        }
+      }
+#pragma unroll
+      for (int k2 = 0; k2 < NT / 2; ++k2)  // 16 keys
+#pragma unroll
+        for (int c = 0; c < VC; ++c) {
+          uint32_t vr[2][2][VW];  // [tile of 8 keys][row 2t + x]
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            lds<VW>(vr[j][0], base + Sh::kTile + v_at0 + c * 128 + (2 * k2 + j) * 8 * ROW);
+            lds<VW>(vr[j][1], base + Sh::kTile + v_at1 + c * 128 + (2 * k2 + j) * 8 * ROW);
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            constexpr int N = HELD8 ? 4 : 2;  // columns of a word
+            uint32_t b[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if constexpr (HELD8) {
+                widen_cols<KIND>(vr[j][0][w], vr[j][1][w], b[j]);
+              } else {
+                b[j][0] = __byte_perm(vr[j][0][w], vr[j][1][w], 0x5410);
+                b[j][1] = __byte_perm(vr[j][0][w], vr[j][1][w], 0x7632);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+              const uint32_t va[4] = {b[0][i], b[0][i + 1], b[1][i], b[1][i + 1]};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma<HALF>(acc[nb][(c * VE + w * N + i) / 2], va, pb[nb][2 * k2], pb[nb][2 * k2 + 1]);
+            }
+          }
+        }
+    }
+
+    // ------------------------------------------------------------ the warps' results
+    cp_wait<0>();
+    __syncthreads();  // the ring's space is reused
+    const float back = HELD8 ? v_ref / kPUp : 1.f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], 4);
+        l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], 8);
+        l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], 16);
+        const int row = warp * NB * 8 + nb * 8 + 2 * t + x;
+        if (g == 0) {
+          sML[row * 2] = m[nb][x];
+          sML[row * 2 + 1] = l[nb][x];
+        }
+        // accumulator i, element e: row 2t + e % 2, column i * 2 + e / 2 of the
+        // lane's: channel c * 8 VE + g * VE + column % VE
+#pragma unroll
+        for (int i = 0; i < MI; i += 2) {
+          const int col = 2 * i, ch = col / VE * 8 * VE + g * VE + col % VE;
+          *reinterpret_cast<float4*>(sO + row * Sh::kOutRow + ch) =
+              make_float4(acc[nb][i][x] * back, acc[nb][i][2 + x] * back, acc[nb][i + 1][x] * back,
+                          acc[nb][i + 1][2 + x] * back);
+        }
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < NB * 8 * D / 4; i += kThreads) {
+      const int r = i / (D / 4), ch = i % (D / 4) * 4;
+      const int rr = r0 + r;
+      if (rr >= n_rows) break;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sML[(w * NB * 8 + r) * 2]);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = sm100::fast_exp2(sML[(w * NB * 8 + r) * 2] - ref);
+        const float4 u = *reinterpret_cast<const float4*>(sO + (w * NB * 8 + r) * Sh::kOutRow + ch);
+        sum = fmaf(f, sML[(w * NB * 8 + r) * 2 + 1], sum);
+        o[0] = fmaf(f, u.x, o[0]);
+        o[1] = fmaf(f, u.y, o[1]);
+        o[2] = fmaf(f, u.z, o[2]);
+        o[3] = fmaf(f, u.w, o[3]);
+      }
+      if (kt0 == 0 && to == kt_n) {
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        const int64_t out = (int64_t)(tok0 + rr / G) * a.Hq + hk * G + rr % G;
+        reinterpret_cast<uint2*>(a.o)[(out * D + ch) / 4] =
+            make_uint2(pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv));
+      } else {
+        // place 0: a block's first piece, which another one began; place 1: its last, which it begins
+        const int64_t at = ((int64_t)blockIdx.x * 2 + (kt0 == 0)) * (8 * NB) + r;
+        *reinterpret_cast<float4*>(a.part_o + at * D + ch) = make_float4(o[0], o[1], o[2], o[3]);
+        if (ch == 0) a.part_ml[at] = make_float2(mm, sum);
+      }
+    }
+    __syncthreads();  // the next piece's ring and query fragments
   }
 }
 
-// Joins the parts of every query row: a block a row, its warps share the
-// parts out and are joined in warp order.
-constexpr int kJoinWarps = 4;
+// Joins the pieces of every query row that lie in several blocks: a block a
+// row, its warps share the pieces out and are joined in warp order.
+constexpr int kJoinWarps = 8;
 template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a, int rows_per_tile, int blocks) {
   __shared__ float sO[kJoinWarps][D];
-  __shared__ float sL[kJoinWarps];
-  __shared__ float sM[kJoinWarps];
-  cudaGridDependencySynchronize();
+  __shared__ float sL[kJoinWarps], sM[kJoinWarps];
+  __shared__ int64_t scratch[kJoinWarps];
   const int64_t out = blockIdx.x;
-  const int tok = (int)(out / a.Hq);
+  const int tok = (int)(out / a.Hq), head = (int)(out % a.Hq), G = a.Hq / a.c.heads;
   int s = tok;
   if (a.q_start) {
     int lo = 0, hi = a.seqs;  // the last sequence whose first token is not after this one
@@ -445,57 +715,76 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
       else hi = mid - 1;
     }
     s = lo;
-    if (s >= a.seqs || __ldg(a.q_start + s) > tok) return;  // a token of no sequence is left as it is
   }
-  const int len = max(0, min(__ldg(a.lens + s), a.width << a.c.log2_page));
-  const int parts = max(1, min(a.splits, (len + a.chunk - 1) / a.chunk));
+  const Seq seq = s < a.seqs ? load_seq(a, s, false) : Seq{0, 0, 0};
+  int64_t before = 0, all = 0;
+  for (int i = threadIdx.x; i < a.seqs; i += kJoinWarps * 32) {
+    const int64_t n = seq_units(a, load_seq(a, i, false), rows_per_tile);
+    all += n;
+    if (i < s) before += n;
+  }
+  all = block_sum<kJoinWarps>(all, scratch);
+  before = block_sum<kJoinWarps>(before, scratch);
+  const int r = (tok - seq.tok0) * G + head % G, kt_n = key_units(seq.len);
+  const int row_tiles = (seq.T * G + rows_per_tile - 1) / rows_per_tile;
+  const int64_t end = before + (int64_t)(head / G * row_tiles + r / rows_per_tile + 1) * kt_n;
+  // block c of nb takes the units [all c / nb, all (c + 1) / nb)
+  const int64_t nb = min((int64_t)blocks, all);
+  auto block_of = [&](int64_t u) { return (int)(((u + 1) * nb + all - 1) / all - 1); };
+  // a token of no sequence is left as it is
+  const bool live = tok >= seq.tok0 && tok < seq.tok0 + seq.T;
+  const int c0 = live ? block_of(end - kt_n + kBegin) : 0, c1 = live ? block_of(end - 1) : 0;
+  cudaGridDependencySynchronize();  // every block: what follows in the stream waits for this kernel alone
+  if (c0 == c1) return;  // written by that block
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float2* ml = a.part_ml + out * a.splits;
+  auto place = [&](int c) { return ((int64_t)c * 2 + (c == c0)) * rows_per_tile + r % rows_per_tile; };
   float mm = -INFINITY;
-  for (int p = threadIdx.x; p < parts; p += kJoinWarps * 32) mm = fmaxf(mm, ml[p].x);
+  for (int c = c0 + threadIdx.x; c <= c1; c += kJoinWarps * 32) mm = fmaxf(mm, a.part_ml[place(c)].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
   if (lane == 0) sM[warp] = mm;
   __syncthreads();
-  mm = fmaxf(fmaxf(sM[0], sM[1]), fmaxf(sM[2], sM[3]));
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, sM[w]);
   const float ref = mm == -INFINITY ? 0.f : mm;
   constexpr int C = D / 32;
   float o[C] = {}, sum = 0.f;
-#pragma unroll 4
-  for (int p = warp; p < parts; p += kJoinWarps) {
-    const float2 x = ml[p];
+#pragma unroll 8
+  for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+    const float2 x = a.part_ml[place(c)];
     const float f = sm100::fast_exp2(x.x - ref);
     sum = fmaf(f, x.y, sum);
-    const float* po = a.part_o + (out * a.splits + p) * D + lane * C;
+    const float* po = a.part_o + place(c) * D + lane * C;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(f, po[c], o[c]);
+    for (int i = 0; i < C; ++i) o[i] = fmaf(f, po[i], o[i]);
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) sO[warp][lane * C + c] = o[c];
+  for (int i = 0; i < C; ++i) sO[warp][lane * C + i] = o[i];
   if (lane == 0) sL[warp] = sum;
   __syncthreads();
-  const float total = (sL[0] + sL[1]) + (sL[2] + sL[3]);
-  const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
-  for (int i = threadIdx.x; i < D / 2; i += kJoinWarps * 32) {
-    float y[2];
+  if (threadIdx.x < D / 2) {
+    float total = 0.f, y[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      y[e] = ((sO[0][2 * i + e] + sO[1][2 * i + e]) + (sO[2][2 * i + e] + sO[3][2 * i + e])) * inv;
-    reinterpret_cast<uint32_t*>(a.o)[out * (D / 2) + i] = pack2<F16>(y[0], y[1]);
+    for (int w = 0; w < kJoinWarps; ++w) {
+      total += sL[w];
+      y[0] += sO[w][2 * threadIdx.x];
+      y[1] += sO[w][2 * threadIdx.x + 1];
+    }
+    const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
+    reinterpret_cast<uint32_t*>(a.o)[out * (D / 2) + threadIdx.x] = pack2<F16>(y[0] * inv, y[1] * inv);
   }
 }
 
-template <int D, int KIND, bool F16>
+template <int D, int KIND, bool F16, int NB>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
-  constexpr int smem = kWarps * 16 * D * 4 + kWarps * 16 * 2 * 4;
-  static_assert(smem <= 48 * 1024, "no opt-in needed");
-  const int64_t row_tiles = ((int64_t)a.max_tokens * (a.Hq / a.c.heads) + 15) / 16;
-  if (row_tiles * a.seqs > 65535) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)a.splits, (unsigned)a.c.heads, (unsigned)(row_tiles * a.seqs));
-  cache_attn_kernel<D, KIND, F16><<<grid, kThreads, smem, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.splits == 1) return e;
-  // the join may be brought up while the parts run; it waits for them itself
+  constexpr int smem = Shape<D, KIND, NB>::kSmem;
+  auto* fn = cache_attn_kernel<D, KIND, F16, NB>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  fn<<<dim3((unsigned)a.blocks), kThreads, smem, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.part_o) return e;
+  // the join may be brought up while the pieces run; it waits for them itself
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.n_tok * a.Hq));
   cfg.blockDim = dim3(kJoinWarps * 32);
@@ -505,36 +794,39 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16>, a);
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16>, a, 8 * NB, a.blocks);
 }
 
+template <int D, int KIND, bool F16>
+cudaError_t by_rows(const CacheAttnArgs& a, cudaStream_t st) {
+  switch (cache_attn_row_tile((int64_t)a.max_tokens * (a.Hq / a.c.heads))) {
+    case 8: return launch<D, KIND, F16, 1>(a, st);
+    case 16: return launch<D, KIND, F16, 2>(a, st);
+    default: return launch<D, KIND, F16, 4>(a, st);
+  }
+}
 template <int D, bool F16>
 cudaError_t by_kind(const CacheAttnArgs& a, cudaStream_t st) {
   switch (a.c.kind) {
-    case LH_CACHE_E4M3: return launch<D, LH_CACHE_E4M3, F16>(a, st);
-    case LH_CACHE_INT8: return launch<D, LH_CACHE_INT8, F16>(a, st);
-    default: return launch<D, F16 ? LH_CACHE_FP16 : LH_CACHE_BF16, F16>(a, st);
+    case LH_CACHE_E4M3: return by_rows<D, LH_CACHE_E4M3, F16>(a, st);
+    case LH_CACHE_INT8: return by_rows<D, LH_CACHE_INT8, F16>(a, st);
+    default: return by_rows<D, F16 ? LH_CACHE_FP16 : LH_CACHE_BF16, F16>(a, st);
   }
 }
 
 }  // namespace
 
-// Parts of a sequence's keys.  Enough blocks for three on each of the 148 SMs
-// (their registers allow three); several sequences have several lengths, and
-// four times as many parts even those out.  A part holds at least 256 keys,
-// so that joining it costs less than reading it.
-void cache_attn_split(int64_t seqs, int64_t kv_heads, int64_t rows, int64_t longest, int* splits, int* chunk) {
-  const int64_t base = seqs * kv_heads * ((rows + 15) / 16);
-  const int64_t want = 444 * (seqs > 1 ? 4 : 1);
-  int64_t n = want / base;
-  const int64_t most = (longest + 255) / 256;
-  if (n > most) n = most;
-  if (n < 1) n = 1;
-  const int64_t unit = kWarps * kKeys;
-  int64_t c = ((longest + n - 1) / n + unit - 1) / unit * unit;
-  if (c < unit) c = unit;
-  *chunk = (int)c;
-  *splits = (int)((longest + c - 1) / c < 1 ? 1 : (longest + c - 1) / c);
+// Blocks of a call and the rows of their places in the workspace: as many
+// blocks as 148 SMs hold at once (three each, two with 32 query rows: their
+// registers), and no more than the units that sequences as long as the table
+// would have.  No sequence has more than one unit of keys: no places.
+void cache_attn_plan(int64_t seqs, int64_t kv_heads, int64_t rows, int64_t longest, int64_t* blocks, int64_t* places) {
+  const int64_t tile = cache_attn_row_tile(rows);
+  const int64_t keys = (longest + kUnit - 1) / kUnit;
+  const int64_t inst = seqs * kv_heads * ((rows + tile - 1) / tile);
+  const int64_t fit = 148 * (tile == 32 ? 2 : 3);
+  *blocks = inst > fit / keys ? fit : inst * keys;
+  *places = keys > 1 ? *blocks * 2 * tile : 0;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int dtype, cudaStream_t st) {

@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* sDel = reinterpret_cast<float*>(smem + Lay::oDel);
     {
       float sum = 0.f;
-      if (q < a.N) {
+      if (NJ != 1 && q < a.N) {
         const uint4* o4 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(O) + b * so.b + h * so.h +
                                                          (int64_t)q * so.n + g * (D / 2));
         const uint4* g4 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(dO) + b * sdo.b +
@@ -596,13 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       sDel[g * 128 + t] = sum;
     }
     compute_sync_q();
-    const float del = sDel[t] + sDel[128 + t];
-    if (g == 0 && q < a.N) a.delta[(int64_t)bh * a.N + q] = del;
+    float del = sDel[t] + sDel[128 + t];
+    if (NJ != 1 && g == 0 && q < a.N) a.delta[(int64_t)bh * a.N + q] = del;
     const float lse_raw = q < a.N ? a.lse[(int64_t)bh * a.N + q] : -INFINITY;
     const float lse = lse_raw == -INFINITY ? INFINITY : lse_raw * kLog2e;  // no key: P = 2^-inf = 0
     const float scale_log2 = a.scale * kLog2e;
     const uint64_t c2 = f2_pack(scale_log2, scale_log2);
-    const uint64_t nl2 = f2_pack(-lse, -lse), d2 = f2_pack(del, del);
+    const uint64_t nl2 = f2_pack(-lse, -lse);
+    uint64_t d2 = f2_pack(del, del);
     const int2 keys = mask_row(a.mask, b, q, a.N);
     const unsigned len = (unsigned)max(0, keys.y - keys.x);
     const Mod mod = MOD ? make_mod(a, h) : Mod{};
@@ -612,7 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kb = (k0 + j) * 128;
       const bool full = kb >= span.max_lo && kb + 128 <= span.min_hi;
       ok = __all_sync(0xffffffffu, mbar_wait(&bS[buf], (j >> 1) & 1, abort_flag));
-      if (!ok) break;
+      if (!ok) {
+        if (NJ == 1) {  // the other warps may be at the two barriers below
+          compute_sync_q();
+          compute_sync_q();
+        }
+        break;
+      }
       tc_fence_after();
       uint32_t r[2][32];
       tmem_ld32(tl + tS + buf * 128 + g * 64, r[0]);
@@ -646,6 +653,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (full) p_pass(std::false_type{});
       else p_pass(std::true_type{});
       ok = __all_sync(0xffffffffu, mbar_wait(bDP, j & 1, abort_flag));
+      if (NJ == 1) {
+        // The row's keys all lie in this tile: Delta = sum_j P dP in fp32
+        // instead of from the rounded O.  With two or three keys, one of them
+        // nearly all of the weight, dP - Delta is a small difference that the
+        // rounding of O would swamp; over more keys it averages out.
+        float sum = 0.f;
+        if (ok) {
+          tc_fence_after();
+          const int lo = keys.x - kb - g * 64;
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t sv[16], dv[16];
+            tmem_ld16(tl + tS + buf * 128 + g * 64 + ch * 16, sv);
+            tmem_ld16(tl + tDP + g * 64 + ch * 16, dv);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x = __uint_as_float(sv[e]) * scale_log2, unused;
+              if constexpr (MOD)
+                x = mod_score(mod, __uint_as_float(sv[e]), (float)(q - kb - g * 64 - ch * 16 - e), unused);
+              if ((unsigned)(ch * 16 + e - lo) < len) sum = fmaf(fast_exp2(x - lse), __uint_as_float(dv[e]), sum);
+            }
+          }
+        }
+        compute_sync_q();  // both halves have read the sums from O
+        sDel[g * 128 + t] = sum;
+        compute_sync_q();
+        del = sDel[t] + sDel[128 + t];
+        d2 = f2_pack(del, del);
+        if (g == 0 && q < a.N) a.delta[(int64_t)bh * a.N + q] = del;
+      }
       if (!ok) break;
       tc_fence_after();
       // dP is released as soon as it is in registers, so that the next

@@ -554,12 +554,12 @@ lh_status lh_cache_read(const lh_cache *cache, int32_t seqs, int32_t width, cons
 
 typedef struct {
   int32_t seqs, width;   /* sequences; columns of the page table */
-  int32_t Hq;            /* query heads, a multiple of the cache's; at most 65535 / 16 sequences x row tiles */
+  int32_t Hq;            /* query heads, a multiple of the cache's */
   int32_t dtype;         /* of q and o: LH_BF16 or LH_FP16; an unquantised cache holds the same type */
   int32_t max_tokens;    /* most query tokens of one sequence (64 with a tree) */
   int64_t n_tok;         /* query tokens of all sequences */
   float scale, softcap;  /* as lh_dense_config */
-  int64_t q_stride[2];   /* token and head strides of q in elements */
+  int64_t q_stride[2];   /* token and head strides of q: multiples of 8 elements (q and o 16-byte aligned) */
 } lh_cache_attn_config;
 
 /* Attention of the newest tokens of each sequence over its cache.  Sequence
