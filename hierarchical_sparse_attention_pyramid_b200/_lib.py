@@ -160,6 +160,6 @@ class LhError(RuntimeError):
 
 
 def call(name: str, *args) -> None:
-    status = getattr(load(), name)(*args)
+    status = getattr(_lib or load(), name)(*args)
     if status != LH_OK:
         raise LhError(status, name)

@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from ._lib import LhCache, LhCacheAttnConfig
-from .dense import _NAMES, _call, _err, _flat, _ptr, _tensor
+from .dense import _NAMES, _call, _err, _flat, _is_tensor, _keep, _plans, _ptr, _sig, _tensor
 
 _KINDS = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float8_e4m3fn: "e4m3", torch.int8: "int8"}
 
@@ -22,6 +22,20 @@ class KVCache:
     8-bit types, k_scale, v_scale [pages, heads, page] fp32.  KVCache.empty allocates them."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
+        _is_tensor("k", k)
+        self.sig = ("cache", _sig(k), _sig(v), _sig(k_scale), _sig(v_scale))
+        plan = _plans.get(self.sig)
+        if plan is None:
+            plan = _keep(self.sig, self._check(k, v, k_scale, v_scale))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page, self.d, self.kind = plan
+        self.device = k.device
+        self.c = LhCache(self.pages, self.page, self.heads, self.d, _lib.CACHE_KINDS[self.kind], k.data_ptr(),
+                         v.data_ptr(), _ptr(k_scale), _ptr(v_scale))
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def _check(k, v, k_scale, v_scale):
         _tensor("k", k)
         if k.dim() != 4 or k.dtype not in _KINDS:
             raise ValueError(f"k: shape {tuple(k.shape)} of {k.dtype}, expected [pages, heads, page, d] of bf16, fp16, "
@@ -33,11 +47,7 @@ class KVCache:
             _flat("v_scale", v_scale, k.device, torch.float32, k.shape[:3])
         elif k_scale is not None or v_scale is not None:
             raise ValueError(f"k_scale, v_scale: a cache of {k.dtype} has none")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.heads, self.page, self.d = k.shape
-        self.kind = _KINDS[k.dtype]
-        self.c = LhCache(self.pages, self.page, self.heads, self.d, _lib.CACHE_KINDS[self.kind], k.data_ptr(),
-                         v.data_ptr(), *(None if t is None else t.data_ptr() for t in (k_scale, v_scale)))
+        return (*k.shape, _KINDS[k.dtype])
 
     @staticmethod
     def empty(pages: int, heads: int, page: int, d: int, kind: str = "e4m3", device="cuda") -> "KVCache":
@@ -46,10 +56,6 @@ class KVCache:
         if dtype.itemsize > 1:
             return KVCache(*kv)
         return KVCache(*kv, *(torch.empty((pages, heads, page), dtype=torch.float32, device=device) for _ in range(2)))
-
-    @property
-    def device(self):
-        return self.k.device
 
 
 def _table(cache: KVCache, page_table):
@@ -62,38 +68,53 @@ def _table(cache: KVCache, page_table):
 def cache_write(cache: KVCache, k, v, slots) -> None:
     """Write tokens k, v [n, heads, d] (bf16, fp16 or fp32, channels contiguous) at slots (int64 [n]: page id * page +
     row; negative: skipped), quantised as the cache holds them.  A slot may be given once in a call."""
-    _tensor("k", k, cache.device)
-    if k.dim() != 3 or tuple(k.shape[1:]) != (cache.heads, cache.d) or k.dtype not in _NAMES:
-        raise ValueError(f"k: shape {tuple(k.shape)} of {k.dtype}, expected [n, {cache.heads}, {cache.d}] of bf16, fp16 "
-                         "or fp32")
-    _tensor("v", v, cache.device, k.dtype, k.shape)
-    _flat("slots", slots, cache.device, torch.int64, k.shape[:1])
-    if k.numel() == 0:
-        return
-    if k.stride(-1) != 1 or v.stride(-1) != 1:
-        raise ValueError("k, v: channels must be contiguous")
-    i2 = ctypes.c_int64 * 2
-    _call("lh_cache_write", cache.device, ctypes.byref(cache.c), k.shape[0], _lib.DENSE_DTYPES[_NAMES[k.dtype]],
-          _ptr(k), _ptr(v), i2(*k.stride()[:2]), i2(*v.stride()[:2]), _ptr(slots), _err(cache.device))
+    for name, t in (("k", k), ("v", v), ("slots", slots)):
+        _is_tensor(name, t)
+    key = ("cache_write", cache.sig, _sig(k), _sig(v), _sig(slots))
+    plan = _plans.get(key)
+    if plan is None:
+        _tensor("k", k, cache.device)
+        if k.dim() != 3 or tuple(k.shape[1:]) != (cache.heads, cache.d) or k.dtype not in _NAMES:
+            raise ValueError(f"k: shape {tuple(k.shape)} of {k.dtype}, expected [n, {cache.heads}, {cache.d}] of bf16, "
+                             "fp16 or fp32")
+        _tensor("v", v, cache.device, k.dtype, k.shape)
+        _flat("slots", slots, cache.device, torch.int64, k.shape[:1])
+        if k.numel() and (k.stride(-1) != 1 or v.stride(-1) != 1):
+            raise ValueError("k, v: channels must be contiguous")
+        i2 = ctypes.c_int64 * 2
+        plan = _keep(key, (k.shape[0], _lib.DENSE_DTYPES[_NAMES[k.dtype]], i2(*k.stride()[:2]), i2(*v.stride()[:2])))
+    n, dtype, k_stride, v_stride = plan
+    if n:
+        index = cache.device.index
+        _call("lh_cache_write", index, cache.ref, n, dtype, k.data_ptr(), v.data_ptr(), k_stride, v_stride,
+              slots.data_ptr(), _err(index))
 
 
 def cache_read(cache: KVCache, page_table, starts, total: int, dtype=torch.bfloat16, out=None):
     """The first starts[s+1] - starts[s] tokens of every sequence s, by its row of page_table (int32 [sequences,
     pages]), in rows starts[s] .. of (k, v) [total, heads, d].  out: (k, v) to write; rows of no sequence are left as
     they are (uninitialised without out)."""
-    seqs, width = _table(cache, page_table)
-    _flat("starts", starts, cache.device, torch.int32, (seqs + 1,))
-    if dtype not in _NAMES:
-        raise ValueError(f"dtype: {dtype}, expected bf16, fp16 or fp32")
-    shape = (total, cache.heads, cache.d)
+    for name, t in (("page_table", page_table), ("starts", starts)):
+        _is_tensor(name, t)
+    key = ("cache_read", cache.sig, _sig(page_table), _sig(starts), total, dtype)
+    plan = _plans.get(key)
+    if plan is None:
+        seqs, width = _table(cache, page_table)
+        _flat("starts", starts, cache.device, torch.int32, (seqs + 1,))
+        if dtype not in _NAMES:
+            raise ValueError(f"dtype: {dtype}, expected bf16, fp16 or fp32")
+        plan = _keep(key, (seqs, width, _lib.DENSE_DTYPES[_NAMES[dtype]], (total, cache.heads, cache.d)))
+    seqs, width, code, shape = plan
     if out is None:
-        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+        out = (torch.empty(shape, dtype=dtype, device=cache.device),
+               torch.empty(shape, dtype=dtype, device=cache.device))
     else:
         for name, t in zip(("out[0]", "out[1]"), out):
             _flat(name, t, cache.device, dtype, shape)
     if total:
-        _call("lh_cache_read", cache.device, ctypes.byref(cache.c), seqs, width, _ptr(page_table), _ptr(starts), total,
-              _lib.DENSE_DTYPES[_NAMES[dtype]], _ptr(out[0]), _ptr(out[1]), _err(cache.device))
+        index = cache.device.index
+        _call("lh_cache_read", index, cache.ref, seqs, width, page_table.data_ptr(), starts.data_ptr(), total, code,
+              out[0].data_ptr(), out[1].data_ptr(), _err(index))
     return out
 
 
@@ -105,6 +126,27 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
     [sequences + 1], first query token of each sequence, at most max_tokens each; None: one each.  A token sees the
     positions up to its own; with tree_mask (int64 [n]) all positions before the sequence's query tokens, and query
     token u of its sequence where bit u is set.  scale, softcap, slopes: as dense_forward."""
+    for name, t in (("q", q), ("page_table", page_table), ("lens", lens)):
+        _is_tensor(name, t)
+    key = ("cache_attention", cache.sig, _sig(q), _sig(page_table), _sig(lens), _sig(q_start), max_tokens,
+           _sig(tree_mask), scale, softcap, _sig(slopes))
+    plan = _plans.get(key)
+    if plan is None:
+        cfg = _attention_config(cache, q, page_table, lens, q_start, max_tokens, tree_mask, scale, softcap, slopes)
+        plan = _keep(key, (cfg, _lib.load().lh_cache_attn_ws_bytes(cache.ref, cfg)))
+    cfg, need = plan
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _flat("out", out, q.device, q.dtype, q.shape)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    index = cache.device.index
+    _call("lh_cache_attn", index, cache.ref, cfg, q.data_ptr(), page_table.data_ptr(), lens.data_ptr(), _ptr(q_start),
+          _ptr(tree_mask), _ptr(slopes), out.data_ptr(), _ptr(ws), need, _err(index))
+    return out
+
+
+def _attention_config(cache, q, page_table, lens, q_start, max_tokens, tree_mask, scale, softcap, slopes):
     seqs, width = _table(cache, page_table)
     _tensor("q", q, cache.device)
     if (q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16) or q.shape[2] != cache.d
@@ -114,7 +156,7 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
     if cache.kind in ("bf16", "fp16") and cache.kind != _NAMES[q.dtype]:
         raise ValueError(f"q: {q.dtype}, expected the cache's {cache.k.dtype}")
     n, Hq, d = q.shape
-    if n and (q.stride(-1) != 1 or q.data_ptr() % 16 or (n > 1 and q.stride(0) % 8) or (Hq > 1 and q.stride(1) % 8)):
+    if n and (q.stride(-1) != 1 or (n > 1 and q.stride(0) % 8) or (Hq > 1 and q.stride(1) % 8)):
         raise ValueError(f"q: strides {q.stride()}, expected contiguous channels in 16-byte rows")
     _flat("lens", lens, cache.device, torch.int32, (seqs,))
     if q_start is not None:
@@ -125,15 +167,6 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
         _flat("tree_mask", tree_mask, cache.device, torch.int64, (n,))
     if slopes is not None:
         _flat("slopes", slopes, cache.device, torch.float32, (Hq,))
-    if out is None:
-        out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
-    else:
-        _flat("out", out, q.device, q.dtype, q.shape)
-    cfg = LhCacheAttnConfig(seqs, width, Hq, _lib.DENSE_DTYPES[_NAMES[q.dtype]], max_tokens, n,
-                            1.0 / math.sqrt(d) if scale is None else scale, softcap,
-                            (ctypes.c_int64 * 2)(q.stride(0), q.stride(1) if Hq > 1 else d))
-    need = _lib.load().lh_cache_attn_ws_bytes(ctypes.byref(cache.c), ctypes.byref(cfg))
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _call("lh_cache_attn", q.device, ctypes.byref(cache.c), ctypes.byref(cfg), _ptr(q), _ptr(page_table), _ptr(lens),
-          _ptr(q_start), _ptr(tree_mask), _ptr(slopes), _ptr(out), _ptr(ws), need, _err(q.device))
-    return out
+    return ctypes.byref(LhCacheAttnConfig(seqs, width, Hq, _lib.DENSE_DTYPES[_NAMES[q.dtype]], max_tokens, n,
+                                          1.0 / math.sqrt(d) if scale is None else scale, softcap,
+                                          (ctypes.c_int64 * 2)(q.stride(0), q.stride(1) if Hq > 1 else d)))

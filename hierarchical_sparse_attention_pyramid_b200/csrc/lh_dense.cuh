@@ -69,7 +69,7 @@ __device__ __forceinline__ TileSpan mask_col_tile(const MaskView& m, int b, int 
 struct SpanBuffer {
   int4 *row_tile, *col_tile;  // [B][n_tiles]
   int2 *rows, *cols;          // [B][N]
-  int* plain_from;            // [B][N] scratch
+  int* scratch;               // [B][N]
 };
 inline SpanBuffer span_buffer(void* p, int64_t B, int64_t N) {
   const int64_t tiles = B * ((N + 127) / 128);
@@ -78,7 +78,7 @@ inline SpanBuffer span_buffer(void* p, int64_t B, int64_t N) {
   s.col_tile = s.row_tile + tiles;
   s.rows = reinterpret_cast<int2*>(s.col_tile + tiles);
   s.cols = s.rows + B * N;
-  s.plain_from = reinterpret_cast<int*>(s.cols + B * N);
+  s.scratch = reinterpret_cast<int*>(s.cols + B * N);
   return s;
 }
 inline size_t span_bytes(int64_t B, int64_t N) {

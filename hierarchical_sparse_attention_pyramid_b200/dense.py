@@ -25,39 +25,60 @@ from ._lib import LhDenseConfig, LhRotaryConfig
 _NAMES = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
 _err_words: dict = {}
 
+# Host plans of the calls (checked configurations), by the tensors' shapes,
+# strides, types and devices and the call's options: a program calls each
+# operator with a handful of those, and checking and filling a configuration
+# takes longer than the smallest kernels run.
+_plans: dict = {}
+_PLANS_MOST = 4096
 
-def _err(device) -> ctypes.c_void_p:
-    """The error word of a device: the calls below report into it (lh_check_error
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _keep(key, plan):
+    if len(_plans) >= _PLANS_MOST:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _err(index: int):
+    """Address of a device's error word: the calls below report into it (lh_check_error
     clears it), see check_dense_error."""
-    t = _err_words.get(device.index)
+    t = _err_words.get(index)
     if t is None:
         if torch.cuda.is_current_stream_capturing():
             return None  # the first call on a device is a captured one: not reported
-        t = _err_words[device.index] = torch.zeros(_lib.ERR_WORD_BYTES, dtype=torch.uint8, device=device)
-        torch.cuda.current_stream(device).synchronize()
-    return ctypes.c_void_p(t.data_ptr())
+        with torch.cuda.device(index):
+            t = torch.zeros(_lib.ERR_WORD_BYTES, dtype=torch.uint8, device="cuda")
+            torch.cuda.current_stream().synchronize()
+        t = _err_words[index] = (t.data_ptr(), t)
+    return t[0]
 
 
 def check_dense_error(device=None) -> None:
     """Synchronise the current stream and raise if a dense attention, rotary or
     cache call on this device reported a timeout or a bad index."""
-    device = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index or 0)
-    if device.index in _err_words:
-        _call("lh_check_error", device, _err(device))
+    index = torch.device("cuda" if device is None else device).index
+    index = torch.cuda.current_device() if index is None else index
+    if index in _err_words:
+        _call("lh_check_error", index, _err(index))
 
 
-def _call(name: str, device, *args) -> None:
+def _call(name: str, index: int, *args) -> None:
     """A library call on a device's current stream (also when another device is current)."""
-    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    if device.index == torch.cuda.current_device():
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
         _lib.call(name, *args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             _lib.call(name, *args, stream)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _tensor(name: str, t, device=None, dtype=None, shape=None):
@@ -75,6 +96,11 @@ def _tensor(name: str, t, device=None, dtype=None, shape=None):
     return t
 
 
+def _is_tensor(name: str, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+
+
 def _flat(name: str, t, device, dtype, shape):
     _tensor(name, t, device, dtype, shape)
     if not t.is_contiguous():
@@ -83,8 +109,8 @@ def _flat(name: str, t, device, dtype, shape):
 
 
 def _addressable(t) -> bool:
-    """Rows of 16-byte units: what the attention kernels can load without a copy."""
-    return (t.stride(-1) == 1 and t.data_ptr() % 16 == 0
+    """Rows of 16-byte units: what the attention kernels can load without a copy (the library checks the pointer)."""
+    return (t.stride(-1) == 1
             and all(n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])))
 
 
@@ -146,11 +172,32 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
     The first 2 * len(frequencies) channels of each head are turned: pairs (i, i + rot/2) with layout "half",
     (2i, 2i + 1) with "interleaved".  positions: int32 [B, N], or None for 0 .. N-1.  inverse turns back: the
     gradient of a call is the inverse call on the output's gradient.  out: (q', k') to write, which may be (q, k)."""
+    ts = (q,) if k is None else (q, k)
+    for name, t in zip(("q", "k"), ts):
+        _is_tensor(name, t)
+    _is_tensor("frequencies", frequencies)
+    if out is None:
+        outs = [torch.empty_like(t) for t in ts]
+    else:
+        outs = list(out)[:len(ts)]
+        for name, o in zip(("out[0]", "out[1]"), outs):
+            _is_tensor(name, o)
+    key = ("rotary", _sig(q), _sig(k), _sig(frequencies), _sig(positions), layout, amplitude, inverse,
+           *((o.shape, o.stride(), o.dtype, o.device) for o in outs))
+    cfg = _plans.get(key)
+    if cfg is None:
+        cfg = _keep(key, _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs))
+    if q.numel() or (k is not None and k.numel()):
+        _call("lh_rotary", q.device.index, cfg, q.data_ptr(), _ptr(k), frequencies.data_ptr(), _ptr(positions),
+              outs[0].data_ptr(), outs[1].data_ptr() if k is not None else None)
+    return outs[0], (outs[1] if k is not None else None)
+
+
+def _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs):
     _tensor("q", q)
     if q.dim() != 4 or q.dtype not in _NAMES:
         raise ValueError(f"q: shape {tuple(q.shape)} of {q.dtype}, expected [B, H, N, d] of bf16, fp16 or fp32")
     B, Hq, N, d = q.shape
-    ts = [q] if k is None else [q, k]
     if k is not None:
         _tensor("k", k, q.device, q.dtype)
         if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
@@ -162,25 +209,17 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
         raise ValueError(f"frequencies: shape {tuple(frequencies.shape)}, expected at most {d // 2} in one row")
     if positions is not None:
         _flat("positions", positions, q.device, torch.int32, (B, N))
-    if out is None:
-        outs = [torch.empty_like(t) for t in ts]
-    else:
-        outs = list(out)[:len(ts)]
-        for name, o, t in zip(("out[0]", "out[1]"), outs, ts):
-            _tensor(name, o, q.device, q.dtype, t.shape)
-    for name, t in zip(("q", "k", "out[0]", "out[1]"), ts + outs):
-        if d > 1 and t.stride(-1) != 1 and t.numel():
-            raise ValueError(f"{name}: channels must be contiguous")
-    for name, o in zip(("out[0]", "out[1]"), outs):
+    for name, o, t in zip(("out[0]", "out[1]"), outs, ts):
+        _tensor(name, o, q.device, q.dtype, t.shape)
         if any(n > 1 and s == 0 for n, s in zip(o.shape, o.stride())):
             raise ValueError(f"{name}: an expanded tensor cannot be written")
-    cfg = LhRotaryConfig(B, N, Hq, 0 if k is None else k.shape[1], d, 2 * frequencies.numel(),
-                         _lib.ROTARY_LAYOUTS[layout], _lib.DENSE_DTYPES[_NAMES[q.dtype]], int(inverse), amplitude,
-                         _strides(q), _strides(ts[-1]), _strides(outs[0]), _strides(outs[-1]))
-    if all(t.numel() for t in ts):
-        _call("lh_rotary", q.device, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(frequencies), _ptr(positions),
-              _ptr(outs[0]), _ptr(outs[1]) if k is not None else None)
-    return outs[0], (outs[1] if k is not None else None)
+    for name, t in zip(("q", "out[0]", "k", "out[1]"), (t for pair in zip(ts, outs) for t in pair)):
+        if d > 1 and t.stride(-1) != 1 and t.numel():
+            raise ValueError(f"{name}: channels must be contiguous")
+    return ctypes.byref(LhRotaryConfig(B, N, Hq, 0 if k is None else k.shape[1], d, 2 * frequencies.numel(),
+                                       _lib.ROTARY_LAYOUTS[layout], _lib.DENSE_DTYPES[_NAMES[q.dtype]], int(inverse),
+                                       amplitude, _strides(q), _strides(ts[-1]), _strides(outs[0]),
+                                       _strides(outs[-1])))
 
 
 class _RotaryFn(torch.autograd.Function):
@@ -221,19 +260,23 @@ def attention_mask(docs=None, prefix=None, causal: bool = True) -> AttentionMask
     some = docs if docs is not None else prefix
     if some is None:
         raise ValueError("attention_mask: docs or prefix needed (a plain causal mask needs none)")
-    _tensor("docs" if docs is not None else "prefix", some)
-    if some.dim() != 2 or some.numel() == 0:
-        raise ValueError(f"docs: shape {tuple(some.shape)}, expected a non-empty [B, N]")
+    _is_tensor("docs" if docs is not None else "prefix", some)
+    key = ("mask", _sig(docs), _sig(prefix))
+    nbytes = _plans.get(key)
+    if nbytes is None:
+        _tensor("docs" if docs is not None else "prefix", some)
+        if some.dim() != 2 or some.numel() == 0:
+            raise ValueError(f"docs: shape {tuple(some.shape)}, expected a non-empty [B, N]")
+        if docs is not None:
+            _flat("docs", docs, some.device, torch.int32, some.shape)
+        if prefix is not None:
+            if prefix.dtype not in (torch.bool, torch.uint8):
+                raise ValueError(f"prefix: dtype {prefix.dtype}, expected bool or uint8")
+            _flat("prefix", prefix, some.device, prefix.dtype, some.shape)
+        nbytes = _keep(key, _lib.load().lh_mask_spans_bytes(*some.shape))
     B, N = some.shape
-    if docs is not None:
-        _flat("docs", docs, some.device, torch.int32, (B, N))
-    if prefix is not None:
-        if prefix.dtype not in (torch.bool, torch.uint8):
-            raise ValueError(f"prefix: dtype {prefix.dtype}, expected bool or uint8")
-        _flat("prefix", prefix, some.device, prefix.dtype, (B, N))
-    spans = torch.empty(_lib.load().lh_mask_spans_bytes(B, N), dtype=torch.uint8, device=some.device)
-    _call("lh_mask_spans", some.device, ctypes.c_int64(B), ctypes.c_int64(N), ctypes.c_int32(bool(causal)), _ptr(docs),
-          _ptr(prefix), _ptr(spans))
+    spans = torch.empty(nbytes, dtype=torch.uint8, device=some.device)
+    _call("lh_mask_spans", some.device.index, B, N, int(bool(causal)), _ptr(docs), _ptr(prefix), spans.data_ptr())
     return AttentionMask(B, N, spans)
 
 
@@ -254,8 +297,7 @@ def _dense_config(q, k, v, mask, causal, scale, softcap, slopes):
     if mask is not None:
         if (mask.B, mask.N) != (B, N):
             raise ValueError(f"mask: of {mask.B} x {mask.N} tokens, expected {B} x {N}")
-        if mask.spans.device != q.device:
-            raise ValueError(f"mask: on {mask.spans.device}, expected {q.device}")
+        _flat("mask.spans", mask.spans, q.device, torch.uint8, (_lib.load().lh_mask_spans_bytes(B, N),))
     if slopes is not None:
         _flat("slopes", slopes, q.device, torch.float32, (Hq,))
     return LhDenseConfig(B, N, Hq, k.shape[1], d, _lib.DENSE_DTYPES[_NAMES[q.dtype]], int(bool(causal)),
@@ -270,43 +312,65 @@ def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = Tru
     mask: from attention_mask (causal is then the mask's); None: causal or full.  scale: 1/sqrt(d) unless given.
     softcap > 0: scores x become softcap * tanh(x / softcap).  slopes: fp32 [Hq], scores get -slope |i - j|.
     A query without keys gets o = 0, lse = -inf."""
-    cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
-    o = torch.empty_like(q)
-    if not _addressable(o):
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    cfg.o_stride = _strides(o)
-    _call("lh_dense_fwd", q.device, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v),
-          None if mask is None else _ptr(mask.spans), _ptr(slopes), _ptr(o), _ptr(lse), _err(q.device))
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _is_tensor(name, t)
+    key = ("dense_forward", _sig(q), _sig(k), _sig(v), None if mask is None else (mask.B, mask.N, _sig(mask.spans)),
+           causal, scale, softcap, _sig(slopes))
+    plan = _plans.get(key)
+    if plan is None:
+        cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
+        o = _like(q)
+        cfg.o_stride = _strides(o)
+        plan = _keep(key, (ctypes.byref(cfg), q.shape[:3], o.stride()))
+    cfg, rows, o_stride = plan
+    o = torch.empty_strided(q.shape, o_stride, dtype=q.dtype, device=q.device)
+    lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+    index = q.device.index
+    _call("lh_dense_fwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          None if mask is None else mask.spans.data_ptr(), _ptr(slopes), o.data_ptr(), lse.data_ptr(), _err(index))
     return o, lse
 
 
 def dense_backward(do, q, k, v, o, lse, mask: AttentionMask | None = None, causal: bool = True,
                    scale: float | None = None, softcap: float = 0.0, slopes=None):
     """Gradients of dense_forward's o with its inputs, o and lse -> (dq, dk, dv)."""
-    cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
-    for name, t in (("do", do), ("o", o)):
-        _tensor(name, t, q.device, q.dtype, q.shape)
-        if not _addressable(t):
-            raise ValueError(f"{name}: strides {t.stride()}, expected contiguous channels in 16-byte rows")
-    _flat("lse", lse, q.device, torch.float32, q.shape[:3])
-    grads = []
-    for n, t in (("dq", q), ("dk", k), ("dv", v)):
-        g = torch.empty_like(t)
-        if not _addressable(g):
-            g = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-        grads.append(g)
-        setattr(cfg, n + "_stride", _strides(g))
-    cfg.o_stride, cfg.do_stride = _strides(o), _strides(do)
-    delta = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _call("lh_dense_bwd", q.device, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse),
-          None if mask is None else _ptr(mask.spans), _ptr(slopes), _ptr(delta), *(_ptr(g) for g in grads),
-          _err(q.device))
-    return tuple(grads)
+    for name, t in (("do", do), ("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse)):
+        _is_tensor(name, t)
+    key = ("dense_backward", _sig(do), _sig(q), _sig(k), _sig(v), _sig(o), _sig(lse),
+           None if mask is None else (mask.B, mask.N, _sig(mask.spans)), causal, scale, softcap, _sig(slopes))
+    plan = _plans.get(key)
+    if plan is None:
+        cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
+        for name, t in (("do", do), ("o", o)):
+            _tensor(name, t, q.device, q.dtype, q.shape)
+            if not _addressable(t):
+                raise ValueError(f"{name}: strides {t.stride()}, expected contiguous channels in 16-byte rows")
+        _flat("lse", lse, q.device, torch.float32, q.shape[:3])
+        grads = [_like(t) for t in (q, k, v)]
+        cfg.o_stride, cfg.do_stride = _strides(o), _strides(do)
+        cfg.dq_stride, cfg.dk_stride, cfg.dv_stride = (_strides(g) for g in grads)
+        plan = _keep(key, (ctypes.byref(cfg), [g.stride() for g in grads]))
+    cfg, strides = plan
+    dq, dk, dv = (torch.empty_strided(t.shape, s, dtype=t.dtype, device=t.device)
+                  for t, s in zip((q, k, v), strides))
+    delta = torch.empty_like(lse)
+    index = q.device.index
+    _call("lh_dense_bwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+          lse.data_ptr(), None if mask is None else mask.spans.data_ptr(), _ptr(slopes), delta.data_ptr(),
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _err(index))
+    return dq, dk, dv
+
+
+def _like(t):
+    """An output like t: with its strides where the kernels can write them."""
+    o = torch.empty_like(t)
+    return o if _addressable(o) else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _usable(t):
-    return t if _addressable(t) else t.contiguous()
+    if _addressable(t) and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 class _DenseAttentionFn(torch.autograd.Function):
