@@ -127,6 +127,53 @@ __device__ __forceinline__ float tanh_abs(float y) {
   return fmaf(-2.f, r, 1.f);
 }
 
+// tanh of 32 scores times `pre`, in place.  Where a warp's are all at most 1
+// in size (scores up to the cap), by the odd polynomial of degree 13 that
+// interpolates tanh(y) / y at Chebyshev points of y^2 in [0, 1]: its error in
+// fp32 arithmetic is 1.3e-7, as large as tanh_abs's, and it needs no
+// exponential or reciprocal, whose unit the softmax's own exponentials fill.
+__device__ __forceinline__ void cap_scores(uint32_t (&r)[32], float pre) {
+  using namespace sm100;
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) top = max3f(top, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+  if (__all_sync(0xffffffffu, top * pre <= 1.f)) {
+    constexpr float c[7] = {0.99999994f, -0.33332857f, 0.13325398f, -0.053465176f, 0.02030552f, -0.00621707f,
+                            0.0010455536f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint64_t y = f2_mul(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_pack(pre, pre));
+      const uint64_t u = f2_mul(y, y);
+      uint64_t p = f2_pack(c[6], c[6]);
+#pragma unroll
+      for (int k = 5; k >= 0; --k) p = f2_fma(p, u, f2_pack(c[k], c[k]));
+      float a, b;
+      f2_unpack(f2_mul(y, p), a, b);
+      r[i] = __float_as_uint(a);
+      r[i + 1] = __float_as_uint(b);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(tanh_abs(__uint_as_float(r[i]) * pre));
+  }
+}
+
+// Capped and biased scores: a score s becomes t = tanh(s pre) (capped, by
+// cap_scores) or s itself, then the exponent of two t mul - slope2 |i - j|.
+struct Mod {
+  float pre, mul, slope2;
+  bool cap, bias;
+};
+__device__ __forceinline__ Mod make_mod(const DenseArgs& a, int h) {
+  Mod m;
+  m.cap = a.softcap > 0.f;
+  m.bias = a.slopes != nullptr;
+  m.pre = m.cap ? a.scale / a.softcap : 0.f;
+  m.mul = (m.cap ? a.softcap : a.scale) * kLog2e;
+  m.slope2 = m.bias ? a.slopes[h] * kLog2e : 0.f;
+  return m;
+}
+
 // 4-D tensor map of a strided 16-bit tensor (with the sequence maps, lh_attn_fwd.cu)
 bool make_head_map(CUtensorMap* m, const void* base, int dtype, int64_t B, int64_t H, int64_t N, int D,
                    const int64_t* stride);

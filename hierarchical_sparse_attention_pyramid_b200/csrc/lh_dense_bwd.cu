@@ -17,7 +17,8 @@
 //   steps over the query tiles that see the key tile, for each query head of
 //   the group.  S^T = K Q_j^T and dP^T = V dO_j^T; P^T and dS^T go back over
 //   the columns they were read from, and dV += P^T dO_j and dK += dS^T Q_j
-//   read them there.
+//   read them there.  Where there are few key tiles, the CTAs of a cluster
+//   share the steps of one and add their sums up in rank order.
 //
 // P and dS enter their products in the inputs' 16-bit type: each rounding is
 // half a step relative to its own value and they are averaged over a row's
@@ -39,33 +40,31 @@ constexpr int kThreadsKV = kComputeKV + 64;
 constexpr int kRegion = 128 * 128;  // one [128 rows][64 x 16 bit] region
 
 __device__ __forceinline__ void compute_sync_kv() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// every thread of every CTA of the cluster; shared memory written before is visible after
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// four floats at this CTA's shared address `at` in the CTA of a rank
+__device__ __forceinline__ float4 ld_cluster(uint32_t at, int rank) {
+  float4 v;
+  uint32_t peer;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void compute_sync_q() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// the scores of 32 columns as exponents of 2, capped and biased: s -> the
-// exponent before LSE, dcap -> 1 - tanh^2
-struct Mod {
-  float pre, cap2, slope2;
-  bool cap, bias;
-};
-__device__ __forceinline__ Mod make_mod(const DenseArgs& a, int h) {
-  Mod m;
-  m.cap = a.softcap > 0.f;
-  m.bias = a.slopes != nullptr;
-  m.pre = m.cap ? a.scale / a.softcap : a.scale * kLog2e;
-  m.cap2 = a.softcap * kLog2e;
-  m.slope2 = m.bias ? a.slopes[h] * kLog2e : 0.f;
-  return m;
-}
-__device__ __forceinline__ float mod_score(const Mod& m, float s, float dist, float& dcap) {
-  float x = s * m.pre;
-  dcap = 1.f;
-  if (m.cap) {
-    const float t = tanh_abs(x);
-    dcap = fmaf(-t, t, 1.f);
-    x = m.cap2 * t;
+// exponents of two of a pair of turned scores, less LSE; d0, d1: distances
+__device__ __forceinline__ void exponents(const Mod& m, float t0, float t1, float l0, float l1, float d0, float d1,
+                                          float& x0, float& x1) {
+  f2_unpack(f2_fma(f2_pack(t0, t1), f2_pack(m.mul, m.mul), f2_pack(-l0, -l1)), x0, x1);
+  if (m.bias) {
+    x0 = fmaf(-m.slope2, fabsf(d0), x0);
+    x1 = fmaf(-m.slope2, fabsf(d1), x1);
   }
-  if (m.bias) x = fmaf(-m.slope2, fabsf(dist), x);
-  return x;
 }
 
 // ===========================================================================
@@ -84,6 +83,9 @@ struct KvSmem {
   static constexpr int oVec = oO + 2 * kTile;  // [2][256] floats: LSE * log2e [128], Delta [128]
   static constexpr int oBar = oVec + 2048;
   static constexpr int kAlloc = oBar + 256;
+  static constexpr int kSumRow = D + 4;        // floats of a row of dV or dK laid over the tiles (padded: 16-byte
+                                               // stores of neighbouring rows meet different banks)
+  static_assert(2 * 128 * kSumRow * 4 <= oVec, "the sums fit over the tiles");
 };
 
 template <int D, bool F16, bool MOD>
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     dense_bwd_kv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                         const __grid_constant__ DenseArgs a, void* __restrict__ dK, const Strides sdk,
-                        void* __restrict__ dV, const Strides sdv) {
+                        void* __restrict__ dV, const Strides sdv, const int C) {
   using Lay = KvSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (reinterpret_cast<uintptr_t>(smem_raw) & 1023) {
@@ -118,13 +120,17 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
   // key-tile-major grid: with a causal mask the first key tiles are seen by
   // the most queries, and the short ones fill the tail
   const int BH = a.B * a.Hkv, G = a.Hq / a.Hkv;
-  const int kt = (int)(blockIdx.x / (unsigned)BH);
-  const int bh = (int)(blockIdx.x % (unsigned)BH);
+  const int rank = (int)(blockIdx.x % (unsigned)C), tile = (int)(blockIdx.x / (unsigned)C);
+  const int kt = tile / BH;
+  const int bh = tile % BH;
   const int b = bh / a.Hkv, hk = bh % a.Hkv;
   const TileSpan span = mask_col_tile(a.mask, b, kt, a.N);
   const int q0 = span.min_lo >> 7;
   const int nq = span.max_hi > span.min_lo ? ((span.max_hi + 127) >> 7) - q0 : 0;
-  const int NJ = nq * G;  // step j: query head hk * G + j / nq, query tile q0 + j % nq
+  // step i of the tile: query head hk * G + i / nq, query tile q0 + i % nq;
+  // this CTA of the cluster takes the steps [i0, i0 + NJ)
+  const int i0 = (int)((int64_t)nq * G * rank / C), NJ = (int)((int64_t)nq * G * (rank + 1) / C) - i0;
+  const int h_first = hk * G + (nq ? i0 / nq : 0), qt_first = q0 + (nq ? i0 % nq : 0);
 
   if (threadIdx.x == 0) {
     mbar_init(bKV, 1);
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         tma_load_4d(smem + Lay::oK + c * kRegion, &tmK, bKV, c * 64, kt * 128, hk, b);
         tma_load_4d(smem + Lay::oV + c * kRegion, &tmV, bKV, c * 64, kt * 128, hk, b);
       }
-      int h = hk * G, qt = q0;
+      int h = h_first, qt = qt_first;
       for (int j = 0; j < NJ; ++j) {
         const int qs = j % 3, os = j & 1;
         if (j >= 3 && !mbar_wait(&bQfree[qs], ((j / 3) - 1) & 1, abort_flag)) break;
@@ -266,7 +272,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
       const int q = qt * 128 + (ct & 127);
       return q < a.N ? ldg_nc_f32((ct < 128 ? a.lse : a.delta) + ((int64_t)b * a.Hq + h) * a.N + q) : -INFINITY;
     };
-    int h = hk * G, qt = q0;
+    int h = h_first, qt = qt_first;
     float vec_next = ct < 256 && NJ > 0 ? vec_raw(h, qt) : 0.f;
     const float scale_log2 = a.scale * kLog2e;
     const uint64_t c2 = f2_pack(scale_log2, scale_log2);
@@ -299,17 +305,17 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         uint32_t sr[32];
         tmem_ld32(tl + tS + g * 32, sr);
         tmem_ld_wait();
+        if (MOD && mod.cap) cap_scores(sr, mod.pre);
         uint32_t ph[16];
         auto p_pass = [&](auto masked) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const int qi = g * 32 + e;
             const float2 l2 = *reinterpret_cast<const float2*>(lse + qi);
-            float pa, pb, da = 1.f, db = 1.f;
+            float pa, pb;
             if constexpr (MOD) {
               const float dist = (float)(qb + qi - kv);
-              pa = mod_score(mod, __uint_as_float(sr[e]), dist, da) - l2.x;
-              pb = mod_score(mod, __uint_as_float(sr[e + 1]), dist + 1.f, db) - l2.y;
+              exponents(mod, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]), l2.x, l2.y, dist, dist + 1.f, pa, pb);
             } else {
               f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, f2_pack(-l2.x, -l2.y)),
                         pa, pb);
@@ -321,13 +327,17 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
               pb = (unsigned)(qi + 1 - lo) < len ? pb : 0.f;
             }
             ph[e >> 1] = pack2<F16>(pa, pb);
-            p[e] = MOD ? pa * da : pa;
-            p[e + 1] = MOD ? pb * db : pb;
+            p[e] = pa;
+            p[e + 1] = pb;
           }
         };
         if (full) p_pass(std::false_type{});
         else p_pass(std::true_type{});
         tmem_st16(tl + tS + g * 32, ph);
+        if (MOD && mod.cap) {  // times 1 - tanh^2
+#pragma unroll
+          for (int e = 0; e < 32; ++e) p[e] = fmaf(-p[e] * __uint_as_float(sr[e]), __uint_as_float(sr[e]), p[e]);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -373,7 +383,14 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
 #pragma unroll
         for (int e = 0; e < CW; ++e) rv[e] = rk[e] = 0u;
       }
-      if (kv < a.N) {
+      if (C > 1) {  // over the tiles, which no product or copy uses any more
+        float* row = reinterpret_cast<float*>(smem) + t * Lay::kSumRow + g * CW;
+#pragma unroll
+        for (int e = 0; e < CW; e += 4) {
+          *reinterpret_cast<uint4*>(row + e) = make_uint4(rv[e], rv[e + 1], rv[e + 2], rv[e + 3]);
+          *reinterpret_cast<uint4*>(row + 128 * Lay::kSumRow + e) = make_uint4(rk[e], rk[e + 1], rk[e + 2], rk[e + 3]);
+        }
+      } else if (kv < a.N) {
         uint4* dv4 = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dV) + b * sdv.b + hk * sdv.h +
                                               (int64_t)kv * sdv.n + g * CW);
         uint4* dk4 = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dK) + b * sdk.b + hk * sdk.h +
@@ -400,6 +417,30 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort_flag) report_error(a.errw, ERRW_TIMEOUT);
+  if (C > 1) {
+    // the cluster's CTAs share out the tile's rows: each sums its rows of dV
+    // and dK over the others' shared memory, in rank order
+    cluster_sync();
+    const int rows = 128 / C;
+    constexpr int Q = D / 4;  // float4s of a row
+    for (int i = threadIdx.x; i < 2 * rows * Q; i += kThreadsKV) {
+      const int which = i / (rows * Q), r = rank * rows + i / Q % rows, c4 = i % Q * 4;
+      const uint32_t at = smem_u32(smem) + (uint32_t)((which * 128 + r) * Lay::kSumRow + c4) * 4;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < C; ++p) {
+        const float4 y = ld_cluster(at, p);
+        x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
+      }
+      const int kv = kt * 128 + r;
+      if (kv < a.N) {
+        const Strides& sd = which ? sdk : sdv;
+        const float f = which ? a.scale : 1.f;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(which ? dK : dV) + b * sd.b + hk * sd.h + (int64_t)kv * sd.n + c4;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(x[0] * f, x[1] * f), pack2<F16>(x[2] * f, x[3] * f));
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  }
 }
 
 // ===========================================================================
@@ -625,6 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tl + tS + buf * 128 + g * 64, r[0]);
       tmem_ld32(tl + tS + buf * 128 + g * 64 + 32, r[1]);
       tmem_ld_wait();
+      if (MOD && mod.cap) {
+        cap_scores(r[0], mod.pre);
+        cap_scores(r[1], mod.pre);
+      }
       float p[2][32];  // P times the cap's derivative
       auto p_pass = [&](auto masked) {
         const int lo = keys.x - kb - g * 64;
@@ -632,11 +677,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float pa, pb, da = 1.f, db = 1.f;
+            float pa, pb;
             if constexpr (MOD) {
               const float dist = (float)(q - kb - g * 64 - ch * 32 - e);
-              pa = mod_score(mod, __uint_as_float(r[ch][e]), dist, da) - lse;
-              pb = mod_score(mod, __uint_as_float(r[ch][e + 1]), dist - 1.f, db) - lse;
+              exponents(mod, __uint_as_float(r[ch][e]), __uint_as_float(r[ch][e + 1]), lse, lse, dist, dist - 1.f, pa,
+                        pb);
             } else {
               f2_unpack(f2_fma(f2_pack(__uint_as_float(r[ch][e]), __uint_as_float(r[ch][e + 1])), c2, nl2), pa, pb);
             }
@@ -646,12 +691,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               pa = (unsigned)(ch * 32 + e - lo) < len ? pa : 0.f;
               pb = (unsigned)(ch * 32 + e + 1 - lo) < len ? pb : 0.f;
             }
-            p[ch][e] = MOD ? pa * da : pa;
-            p[ch][e + 1] = MOD ? pb * db : pb;
+            p[ch][e] = pa;
+            p[ch][e + 1] = pb;
           }
       };
       if (full) p_pass(std::false_type{});
       else p_pass(std::true_type{});
+      if (MOD && mod.cap) {  // times 1 - tanh^2
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            p[ch][e] = fmaf(-p[ch][e] * __uint_as_float(r[ch][e]), __uint_as_float(r[ch][e]), p[ch][e]);
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(bDP, j & 1, abort_flag));
       if (NJ == 1) {
         // The row's keys all lie in this tile: Delta = sum_j P dP in fp32
@@ -670,9 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float x = __uint_as_float(sv[e]) * scale_log2, unused;
-              if constexpr (MOD)
-                x = mod_score(mod, __uint_as_float(sv[e]), (float)(q - kb - g * 64 - ch * 16 - e), unused);
+              float x = __uint_as_float(sv[e]) * (MOD ? mod.mul : scale_log2);
+              if constexpr (MOD) {
+                if (mod.cap) x = tanh_abs(__uint_as_float(sv[e]) * mod.pre) * mod.mul;
+                if (mod.bias) x = fmaf(-mod.slope2, fabsf((float)(q - kb - g * 64 - ch * 16 - e)), x);
+              }
               if ((unsigned)(ch * 16 + e - lo) < len) sum = fmaf(fast_exp2(x - lse), __uint_as_float(dv[e]), sum);
             }
           }
@@ -764,8 +818,21 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   fq<<<dim3((unsigned)gq), kThreads, QSmem<D>::kAlloc, st>>>(q, k, v, go, a, o, so, dout, sdo, dq, sdq);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fk<<<dim3((unsigned)gk), kThreadsKV, KvSmem<D>::kAlloc, st>>>(q, k, v, go, a, dk, sdk, dv, sdv);
-  return cudaGetLastError();
+  // few key tiles leave SMs idle: then a cluster of 2, 4 or 8 CTAs shares the
+  // query steps of one, as long as a wave of 148 holds them
+  int C = 1;
+  while (C < 8 && gk * C * 2 <= 148 && (int64_t)a.n_tiles * (a.Hq / a.Hkv) >= 2 * C) C *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(gk * C));
+  cfg.blockDim = dim3(kThreadsKV);
+  cfg.dynamicSmemBytes = KvSmem<D>::kAlloc;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {(unsigned)C, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fk, q, k, v, go, a, dk, sdk, dv, sdv, C);
 }
 
 }  // namespace

@@ -40,7 +40,7 @@ struct Smem {
 };
 
 // MOD: scores are capped or biased (they are turned once and written back to
-// TMEM in the log2 domain with the masked ones at -inf)
+// TMEM, the masked ones as -inf)
 template <int D, bool F16, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -178,10 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = tl + x * 128, to = tl + 256 + x * D;
     const int2 keys = mask_row(a.mask, b, row, a.N);
-    const float scale_log2 = MOD ? 1.f : a.scale * kLog2e;
-    const float slope2 = MOD && a.slopes ? a.slopes[h] * kLog2e : 0.f;
-    const float cap2 = MOD ? a.softcap * kLog2e : 0.f;
-    const float pre = MOD ? (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e) : 0.f;
+    const Mod mod = MOD ? make_mod(a, h) : Mod{};
+    const float scale_log2 = !MOD ? a.scale * kLog2e : mod.bias ? 1.f : mod.mul;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = first[x]; j < end[x]; ++j) {
@@ -204,19 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (MOD) {
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
-            if (a.softcap > 0.f) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                r[ch][i] = __float_as_uint(cap2 * tanh_abs(__uint_as_float(r[ch][i]) * pre));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[ch][i] = __float_as_uint(__uint_as_float(r[ch][i]) * pre);
-            }
-            if (a.slopes) {
+            if (mod.cap) cap_scores(r[ch], mod.pre);
+            if (mod.bias) {
               const float d0 = (float)(row - j * 128 - hh * 64 - ch * 32);  // distance to key 0 of the chunk
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                r[ch][i] = __float_as_uint(fmaf(-slope2, fabsf(d0 - (float)i), __uint_as_float(r[ch][i])));
+                r[ch][i] = __float_as_uint(
+                    fmaf(-mod.slope2, fabsf(d0 - (float)i), __uint_as_float(r[ch][i]) * mod.mul));
             }
             if (!full) {
 #pragma unroll
