@@ -12,8 +12,8 @@
 //   warp 9          MMA issuer: per key tile P_A V, the next S_A = Q_A K^T,
 //                   P_B V, the next S_B
 // TMEM columns: S_A/P_A [0,128), S_B/P_B [128,256), O_A [256,256+D),
-// O_B [256+D,256+2D).  P goes back over the first 64 of the S columns it came
-// from, in the inputs' 16-bit type: its rounding (half a step, 2^-9 in bf16)
+// O_B [256+D,256+2D).  P goes back over the first half of the 64 S columns it
+// came from, in the inputs' 16-bit type: its rounding (half a step, 2^-9 in bf16)
 // is averaged over the row's keys and stays below the rounding of O itself.
 // The sums, the maximum, O and LSE are fp32.
 #include <type_traits>
@@ -27,6 +27,10 @@ using namespace sm100;
 constexpr int kSoftmax = 256;
 constexpr int kThreads = kSoftmax + 64;
 constexpr int kWarpTma = 8, kWarpMma = 9;
+// every kPolyOf-th pair of exponentials of an unmasked tile goes to the FMA
+// pipes: the exponential unit makes 16 a clock and SM, 2048 clocks for the two
+// query tiles' 2 x 128 x 128, as long as their matrix products take
+constexpr int kPolyOf = 3;
 constexpr int kRegion = 128 * 128;  // one [128 rows][64 x 16 bit] region
 
 template <int D>
@@ -55,8 +59,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bV = bars + 3;       // [2]
   uint64_t* bKVfree = bars + 5;  // [2]
   uint64_t* bS = bars + 7;       // [2] tiles: S in TMEM (and the tile's previous P V done)
-  uint64_t* bP = bars + 9;       // [2] tiles: P in TMEM, O rescaled (128 arrivals)
-  uint64_t* bO = bars + 11;      // [2] tiles: a P V product done
+  uint64_t* bP = bars + 9;       // [2] tiles x [2] halves of the keys: P in TMEM (128 arrivals); O rescaled
+  uint64_t* bO = bars + 13;      // [2] tiles: a P V product done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::oBar + 192);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::oBar + 196);
 
@@ -90,7 +94,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bV[s], 1);
       mbar_init(&bKVfree[s], 1);
       mbar_init(&bS[s], 1);
-      mbar_init(&bP[s], 128);
+      mbar_init(&bP[2 * s], 128);
+      mbar_init(&bP[2 * s + 1], 128);
       mbar_init(&bO[s], 1);
     }
     *abort_flag = 0;
@@ -141,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = mbar_wait_warp(bQ, 0, abort_flag) && mbar_wait_warp(&bK[0], 0, abort_flag);
       if (ok) {
         tc_fence_after();
+#pragma unroll
         for (int x = 0; x < 2; ++x)
           if (first[x] == j0 && end[x] > j0) issue_s(x, j0);
       }
@@ -150,15 +156,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // reads it, so that a stage is never refilled under a copy
         ok = mbar_wait_warp(&bV[st], (i >> 1) & 1, abort_flag);
         bool k_next = false;
-        for (int x = 0; x < 2 && ok; ++x) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok) break;
           if (j >= first[x] && j < end[x]) {
-            if (!mbar_wait_warp(&bP[x], (j - first[x]) & 1, abort_flag)) { ok = false; break; }
-            tc_fence_after();
             const uint64_t vb = mV + ((st * Lay::kTile) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_tmem_a_w(tmem + 256 + x * D, tmem + x * 128 + kk * 8, vb + ((kk * 2048) >> 4), idPV,
-                                 (j > first[x] || kk > 0) ? 1u : 0u);
+            for (int half = 1; half >= 0; --half) {  // keys 64-127 come first
+              if (!mbar_wait_warp(&bP[2 * x + half], (j - first[x]) & 1, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16_tmem_a_w(tmem + 256 + x * D, tmem + x * 128 + half * 64 + kk * 8,
+                                   vb + (((half * 4 + kk) * 2048) >> 4), idPV,
+                                   (j > first[x] || half == 0 || kk > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
             umma_commit_w(&bO[x]);
           }
           if (j + 1 < j1 && !k_next) {
@@ -174,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax
     const int x = warp >> 2;
+    const int j_first = x ? first[1] : first[0], j_end = x ? end[1] : end[0];
+    const TileSpan sp = x ? span[1] : span[0];
     const int row = (2 * c + x) * 128 + (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = tl + x * 128, to = tl + 256 + x * D;
@@ -182,11 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale_log2 = !MOD ? a.scale * kLog2e : mod.bias ? 1.f : mod.mul;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    for (int j = first[x]; j < end[x]; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&bS[x], (j - first[x]) & 1, abort_flag));
+    for (int j = j_first; j < j_end; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bS[x], (j - j_first) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      const bool full = j * 128 >= span[x].max_lo && j * 128 + 128 <= span[x].min_hi;
+      const bool full = j * 128 >= sp.max_lo && j * 128 + 128 <= sp.min_hi;
       const int lo = keys.x - j * 128;
       const unsigned len = (unsigned)max(0, keys.y - keys.x);
       // row maximum over two 64-key halves, in eight independent chains
@@ -243,42 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float m_new = move ? m_tile : m_run;
       const float alpha = move ? fast_exp2(m_run - m_new) : 1.f;
       const float m_ref = m_new == -INFINITY ? 0.f : m_new;  // no key of the row so far: every P is 0
-      const uint64_t c2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m_ref, -m_ref);
-      uint64_t rs2[4];
-      auto p_pass = [&](auto masked) {
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          tmem_ld32(ts + hh * 64, r[0]);
-          tmem_ld32(ts + hh * 64 + 32, r[1]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            const int ch = hh * 2 + cc;
-            rs2[ch] = f2_pack(0.f, 0.f);
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float pa, pb;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(r[cc][e]), __uint_as_float(r[cc][e + 1])), c2, nm2), pa, pb);
-              pa = fast_exp2(pa);
-              pb = fast_exp2(pb);
-              if constexpr (decltype(masked)::value) {
-                pa = (unsigned)(ch * 32 + e - lo) < len ? pa : 0.f;
-                pb = (unsigned)(ch * 32 + e + 1 - lo) < len ? pb : 0.f;
-              }
-              rs2[ch] = f2_add(rs2[ch], f2_pack(pa, pb));
-              pk[e >> 1] = pack2<F16>(pa, pb);
-            }
-            tmem_st16(ts + ch * 16, pk);
-          }
-        }
-      };
-      if (!MOD && !full) p_pass(std::true_type{});
-      else p_pass(std::false_type{});
-      float rsa, rsb;
-      f2_unpack(f2_add(f2_add(rs2[0], rs2[1]), f2_add(rs2[2], rs2[3])), rsa, rsb);
       // rescale the O row (the tile's previous P V completed before this S)
-      if (j > first[x] && __any_sync(0xffffffffu, move)) {
+      if (j > j_first && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t o[32];
@@ -289,14 +270,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(to + ch * 32, o);
         }
       }
+      // P over the S columns that each half of the keys came from; the half
+      // that the maximum read last is still in registers and goes first, and
+      // its P V starts while the other half's P is made
+      const uint64_t c2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m_ref, -m_ref);
+      uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+      auto p_chunk = [&](auto masked, uint32_t (&sv)[32], int key, uint32_t dst, uint64_t& sum) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nm2);
+          float pa, pb;
+          if constexpr (decltype(masked)::value) {
+            f2_unpack(x2, pa, pb);
+            pa = (unsigned)(key + e - lo) < len ? fast_exp2(pa) : 0.f;
+            pb = (unsigned)(key + e + 1 - lo) < len ? fast_exp2(pb) : 0.f;
+          } else if (!MOD && (e >> 1) % kPolyOf == kPolyOf - 1) {
+            poly_exp2(x2, pa, pb);
+          } else {
+            f2_unpack(x2, pa, pb);
+            pa = fast_exp2(pa);
+            pb = fast_exp2(pb);
+          }
+          sum = f2_add(sum, f2_pack(pa, pb));
+          pk[e >> 1] = pack2<F16>(pa, pb);
+        }
+        tmem_st16(dst, pk);
+      };
+      auto p_pass = [&](auto masked) {
+        p_chunk(masked, r[0], 64, ts + 64, rs2[0]);
+        tmem_ld32(ts, r[0]);
+        p_chunk(masked, r[1], 96, ts + 80, rs2[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bP[2 * x + 1]);
+        tmem_ld_wait32(r[0]);
+        tmem_ld32(ts + 32, r[1]);
+        p_chunk(masked, r[0], 0, ts, rs2[0]);
+        tmem_ld_wait32(r[1]);
+        p_chunk(masked, r[1], 32, ts + 16, rs2[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bP[2 * x]);
+      };
+      if (!MOD && !full) p_pass(std::true_type{});
+      else p_pass(std::false_type{});
+      float rsa, rsb;
+      f2_unpack(f2_add(rs2[0], rs2[1]), rsa, rsb);
       l_run = l_run * alpha + (rsa + rsb);
       m_run = m_new;
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&bP[x]);
     }
-    const bool any = end[x] > first[x];
-    if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(&bO[x], (end[x] - first[x] - 1) & 1, abort_flag));
+    const bool any = j_end > j_first;
+    if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(&bO[x], (j_end - j_first - 1) & 1, abort_flag));
     if (ok && (x == 0 || hasB)) {
       tc_fence_after();
       const float inv_l = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;

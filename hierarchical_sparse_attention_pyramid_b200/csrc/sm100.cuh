@@ -190,6 +190,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// the same, for 32 registers of a load whose wait does not follow it at once:
+// nothing that uses them moves before the wait
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]));
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- MMA
@@ -255,6 +265,27 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+// 2^x of a pair on the FMA pipes (x <= 127; below -126 it returns 2^-126):
+// x = n + f with n the nearest integer, 2^f by the polynomial of degree 4
+// that interpolates it at Chebyshev points of [-1/2, 1/2] (relative error
+// 4e-6), n added to the exponent bits
+__device__ __forceinline__ void poly_exp2(uint64_t x, float& a, float& b) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  x = f2_pack(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
+  const uint64_t magic = f2_pack(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low bits are n
+  const uint64_t n = f2_add(x, magic);
+  const uint64_t f = f2_sub(x, f2_sub(n, magic));
+  constexpr float c[5] = {1.00000012f, 0.693121016f, 0.240221068f, 0.0559220351f, 0.00967603736f};
+  uint64_t p = f2_pack(c[4], c[4]);
+#pragma unroll
+  for (int k = 3; k >= 0; --k) p = f2_fma(p, f, f2_pack(c[k], c[k]));
+  float na, nb;
+  f2_unpack(n, na, nb);
+  f2_unpack(p, a, b);
+  a = __uint_as_float(__float_as_uint(na) * 8388608u + __float_as_uint(a));
+  b = __uint_as_float(__float_as_uint(nb) * 8388608u + __float_as_uint(b));
 }
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
