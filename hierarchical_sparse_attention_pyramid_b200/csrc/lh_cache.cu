@@ -100,24 +100,22 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
 template <typename T, int KIND, int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheIoArgs a) {
   constexpr int LANES = D / 8;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int lane = (int)(id % LANES);
-  const int64_t r = id / LANES;
-  const int64_t tok = r / a.c.heads;
-  const int h = (int)(r % a.c.heads);
-  // every lane reaches the shuffles; rows that are not written compute on zeros
+  const int lane = threadIdx.x % LANES;
+  const uint32_t r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;  // token * heads + head
+  const uint32_t tok = r / (uint32_t)a.c.heads;
+  const int h = (int)(r % (uint32_t)a.c.heads);
+  // every lane reaches the shuffles; rows that are not written compute on
+  // zeros.  The rows are loaded beside their slot, not after it.
+  float k[8] = {}, v[8] = {};
   int64_t slot = -1;
   if (tok < a.n) {
-    slot = a.slots[tok];
+    slot = __ldg(a.slots + tok);
+    load8<T, WIDE>(static_cast<const T*>(a.k) + tok * a.k_stride[0] + h * a.k_stride[1] + lane * 8, k);
+    load8<T, WIDE>(static_cast<const T*>(a.v) + tok * a.v_stride[0] + h * a.v_stride[1] + lane * 8, v);
     if (slot >= a.c.pages << a.c.log2_page) {
       if (lane == 0) report_error(a.errw, ERRW_BOUNDS);
       slot = -1;
     }
-  }
-  float k[8] = {}, v[8] = {};
-  if (slot >= 0) {
-    load8<T, WIDE>(static_cast<const T*>(a.k) + tok * a.k_stride[0] + h * a.k_stride[1] + lane * 8, k);
-    load8<T, WIDE>(static_cast<const T*>(a.v) + tok * a.v_stride[0] + h * a.v_stride[1] + lane * 8, v);
   }
   const int64_t page = slot >> a.c.log2_page, at = slot & ((1 << a.c.log2_page) - 1);
   const int64_t row = ((page * a.c.heads + h) << a.c.log2_page) + at;
@@ -179,9 +177,8 @@ template <typename T, int KIND, int D>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoArgs a) {
   constexpr int BYTES = KIND == LH_CACHE_E4M3 || KIND == LH_CACHE_INT8 ? 1 : 2;
   constexpr int V = 16 / BYTES, LANES = D / V;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int lane = (int)(id % LANES);
-  const int64_t r = id / LANES;
+  const int lane = threadIdx.x % LANES;
+  const uint32_t r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
   const int per = (a.c.heads + gridDim.y - 1) / gridDim.y;
   const int h0 = blockIdx.y * per, h1 = min(h0 + per, a.c.heads);
   if (r >= a.n) return;
@@ -195,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoArgs 
     return;
   }
   const int64_t at = pos & ((1 << a.c.log2_page) - 1);
-#pragma unroll 2
+#pragma unroll 4
   for (int h = h0; h < h1; ++h) {
     const int64_t row = (((int64_t)page * a.c.heads + h) << a.c.log2_page) + at;
     float ks = 1.f, vs = 1.f;
@@ -203,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoArgs 
       ks = __ldg(a.c.k_scale + row);
       vs = __ldg(a.c.v_scale + row);
     }
-    const int64_t src = (row * D + lane * V) * BYTES, dst = (r * a.c.heads + h) * D + lane * V;
+    const int64_t src = (row * D + lane * V) * BYTES, dst = ((int64_t)r * a.c.heads + h) * D + lane * V;
     widen<T, KIND, V>(static_cast<const char*>(a.c.k) + src, ks, static_cast<T*>(a.k_out) + dst);
     widen<T, KIND, V>(static_cast<const char*>(a.c.v) + src, vs, static_cast<T*>(a.v_out) + dst);
   }
@@ -211,8 +208,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoArgs 
 
 template <typename T, int KIND, int D>
 cudaError_t write_d(const CacheIoArgs& a, cudaStream_t st) {
-  const int64_t grid = (a.n * a.c.heads * (D / 8) + kThreads - 1) / kThreads;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  constexpr int R = kThreads / (D / 8);  // rows of a block
+  const int64_t grid = (a.n * a.c.heads + R - 1) / R;
   constexpr int64_t W = 16 / sizeof(T);
   const bool wide = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0 &&
                     a.k_stride[0] % W == 0 && a.k_stride[1] % W == 0 && a.v_stride[0] % W == 0 &&
@@ -225,8 +222,8 @@ cudaError_t write_d(const CacheIoArgs& a, cudaStream_t st) {
 template <typename T, int KIND, int D>
 cudaError_t read_d(const CacheIoArgs& a, cudaStream_t st) {
   constexpr int V = KIND == LH_CACHE_E4M3 || KIND == LH_CACHE_INT8 ? 16 : 8;
-  const int64_t gx = (a.n * (D / V) + kThreads - 1) / kThreads;
-  if (gx > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  constexpr int R = kThreads / (D / V);  // tokens of a block
+  const int64_t gx = (a.n + R - 1) / R;
   // a thread walks the heads of its token (one page lookup); with few tokens
   // the heads are shared out until there are four blocks an SM
   int gy = (int)(592 / gx);

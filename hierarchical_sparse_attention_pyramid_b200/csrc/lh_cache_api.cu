@@ -84,7 +84,7 @@ lh_status lh_cache_write(const lh_cache* cache, int64_t n, int32_t dtype, const 
   if (s != LH_OK) return s;
   if (dtype != LH_BF16 && dtype != LH_FP16 && dtype != LH_FP32) return fail(LH_ERR_INVALID_ARG, kCall, "bad dtype");
   if (n < 0) return fail(LH_ERR_INVALID_ARG, kCall, "negative token count");
-  if (n > ((int64_t)1 << 40)) return fail(LH_ERR_UNSUPPORTED, kCall, "too many tokens");
+  if (n > 0x7fffffffll / cache->heads) return fail(LH_ERR_UNSUPPORTED, kCall, "2^31 rows or more");
   if (n == 0) return LH_OK;
   const uintptr_t elem = dtype == LH_FP32 ? 4 : 2;
   if (!k || !v || !slots || !k_stride || !v_stride || !aligned(k, elem) || !aligned(v, elem) || !aligned(slots, 8) ||

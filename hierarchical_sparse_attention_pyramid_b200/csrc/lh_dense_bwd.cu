@@ -818,10 +818,14 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   fq<<<dim3((unsigned)gq), kThreads, QSmem<D>::kAlloc, st>>>(q, k, v, go, a, o, so, dout, sdo, dq, sdq);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // few key tiles leave SMs idle: then a cluster of 2, 4 or 8 CTAs shares the
-  // query steps of one, as long as a wave of 148 holds them
+  // Few key tiles leave SMs idle: then a cluster of 2, 4 or 8 CTAs shares the
+  // query steps of one, as long as a wave of 148 holds them (257 tokens, 2 key
+  // heads of 4 query heads each: 47 us without, 14 with).  Up to two waves of
+  // tiles of unequal length pair up (8K tokens in documents, 256 tiles: 149 us
+  // without, 133 with clusters of 2, 178 of 4).
   int C = 1;
   while (C < 8 && gk * C * 2 <= 148 && (int64_t)a.n_tiles * (a.Hq / a.Hkv) >= 2 * C) C *= 2;
+  if (C == 1 && gk <= 296 && (int64_t)a.n_tiles * (a.Hq / a.Hkv) >= 2) C = 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(gk * C));
   cfg.blockDim = dim3(kThreadsKV);

@@ -30,7 +30,7 @@ constexpr int kWarpTma = 8, kWarpMma = 9;
 // every kPolyOf-th pair of exponentials of an unmasked tile goes to the FMA
 // pipes: the exponential unit makes 16 a clock and SM, 2048 clocks for the two
 // query tiles' 2 x 128 x 128, as long as their matrix products take
-constexpr int kPolyOf = 3;
+constexpr int kPolyOf = 4;
 constexpr int kRegion = 128 * 128;  // one [128 rows][64 x 16 bit] region
 
 template <int D>
