@@ -2,8 +2,8 @@
 // reading sequences back.
 //
 // Both are bound by memory (each element moves once in each direction).  A
-// row is one token's head: d/8 lanes of 8 channels each when writing, so that
-// the row's largest magnitude is a shuffle reduction, and 16 bytes of held
+// row is one token's head: d/16 lanes of 16 channels each when writing, so
+// that the row's largest magnitude is a shuffle reduction, and 16 bytes of held
 // values a lane when reading.  A thread carries K and V together, which keeps
 // two rows' loads in flight and looks the page up once for both.
 #include <cuda_fp8.h>
@@ -17,6 +17,8 @@ namespace lh {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kV = 16;         // channels of a lane when writing (8: 60 us instead of 48 for 87K tokens of 4 heads)
+constexpr int kReadHeads = 2;  // heads that a thread reads (1, 4: 52, 55 us instead of 50)
 
 template <typename T> __device__ __forceinline__ float to_f(T x);
 template <> __device__ __forceinline__ float to_f<float>(float x) { return x; }
@@ -27,9 +29,10 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+// largest size of three, NaN if one is NaN
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -38,80 +41,88 @@ struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Pack {
   T e[N];
 };
 
-// x (8 channels of a lane) of a row of LANES lanes into the cache; every lane
+// x (16 channels of a lane) of a row of LANES lanes into the cache; every lane
 // of the warp calls it, the rows that are `live` are stored
 template <int KIND, int LANES>
-__device__ __forceinline__ void store_row(const float (&x)[8], void* data, float* scale, int64_t row, int lane_in_row,
+__device__ __forceinline__ void store_row(const float (&x)[kV], void* data, float* scale, int64_t row, int lane_in_row,
                                           bool live) {
   if constexpr (KIND == LH_CACHE_BF16 || KIND == LH_CACHE_FP16) {
     using H = typename std::conditional<KIND == LH_CACHE_BF16, __nv_bfloat16, __half>::type;
-    Pack<H, 8> p;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p.e[i] = from_f<H>(x[i]);
-    if (live) reinterpret_cast<Pack<H, 8>*>(data)[row * LANES + lane_in_row] = p;
+    for (int j = 0; j < 2; ++j) {
+      Pack<H, 8> p;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p.e[i] = from_f<H>(x[8 * j + i]);
+      if (live) reinterpret_cast<Pack<H, 8>*>(data)[(row * LANES + lane_in_row) * 2 + j] = p;
+    }
   } else {
     constexpr float top = KIND == LH_CACHE_E4M3 ? 448.f : 127.f;
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+    for (int i = 0; i < kV; i += 2) m = max_abs3(m, x[i], x[i + 1]);
 #pragma unroll
-    for (int d = LANES / 2; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = LANES / 2; d > 0; d >>= 1) m = max_abs3(m, m, __shfl_xor_sync(0xffffffffu, m, d));
     const bool finite = m <= 3.402823466e38f;
     // a row below about 1e-36 would need a multiplier beyond fp32: the largest one is used
     const float inv = m > 0.f ? fminf(__fdiv_rn(top, m), 3.402823466e38f) : 0.f;
-    uint64_t w = 0;
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float a = __fmul_rn(x[i], inv), b = __fmul_rn(x[i + 1], inv);
-      uint32_t h;
-      if constexpr (KIND == LH_CACHE_E4M3) {
-        h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-      } else {
-        const int ia = __float2int_rn(fminf(fmaxf(a, -top), top)), ib = __float2int_rn(fminf(fmaxf(b, -top), top));
-        h = (uint32_t)(ia & 0xff) | (uint32_t)(ib & 0xff) << 8;
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = __fmul_rn(x[4 * j + 2 * i], inv), b = __fmul_rn(x[4 * j + 2 * i + 1], inv);
+        if constexpr (KIND == LH_CACHE_E4M3) {
+          h[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        } else {
+          const int ia = __float2int_rn(fminf(fmaxf(a, -top), top)), ib = __float2int_rn(fminf(fmaxf(b, -top), top));
+          h[i] = __byte_perm(ia, ib, 0x0040);
+        }
       }
-      w |= (uint64_t)h << (8 * i);
+      w[j] = __byte_perm(h[0], h[1], 0x5410);
     }
     // a row with a NaN or an infinity reads back as NaN
-    if (!finite) w = 0;
-    if (live) reinterpret_cast<uint64_t*>(data)[row * LANES + lane_in_row] = w;
-    if (live && lane_in_row == 0) scale[row] = finite ? __fdiv_rn(m, top) : __int_as_float(0x7fffffff);
+    if (live) {
+      reinterpret_cast<uint4*>(data)[row * LANES + lane_in_row] = finite ? make_uint4(w[0], w[1], w[2], w[3])
+                                                                         : make_uint4(0, 0, 0, 0);
+      if (lane_in_row == 0) scale[row] = finite ? __fdiv_rn(m, top) : __int_as_float(0x7fffffff);
+    }
   }
 }
 
 template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (WIDE) {
-    Pack<T, 16 / sizeof(T)> u[sizeof(T) * 8 / 16];
+__device__ __forceinline__ void load_row(const T* p, float (&x)[kV]) {
+  constexpr int N = 16 / sizeof(T);
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      u[i] = *reinterpret_cast<const Pack<T, 16 / sizeof(T)>*>(&v);
+  for (int j = 0; j < kV / N; ++j) {
+    if constexpr (WIDE) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[N * j + i] = to_f<T>(e[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[N * j + i] = to_f<T>(p[N * j + i]);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f<T>(u[i / (16 / sizeof(T))].e[i % (16 / sizeof(T))]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f<T>(p[i]);
   }
 }
 
 // WIDE: 16-byte loads (pointers and strides allow them)
 template <typename T, int KIND, int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheIoArgs a) {
-  constexpr int LANES = D / 8;
+  constexpr int LANES = D / kV;
   const int lane = threadIdx.x % LANES;
   const uint32_t r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;  // token * heads + head
   const uint32_t tok = r / (uint32_t)a.c.heads;
   const int h = (int)(r % (uint32_t)a.c.heads);
   // every lane reaches the shuffles; rows that are not written compute on
   // zeros.  The rows are loaded beside their slot, not after it.
-  float k[8] = {}, v[8] = {};
+  float k[kV] = {}, v[kV] = {};
   int64_t slot = -1;
   if (tok < a.n) {
     slot = __ldg(a.slots + tok);
-    load8<T, WIDE>(static_cast<const T*>(a.k) + tok * a.k_stride[0] + h * a.k_stride[1] + lane * 8, k);
-    load8<T, WIDE>(static_cast<const T*>(a.v) + tok * a.v_stride[0] + h * a.v_stride[1] + lane * 8, v);
+    load_row<T, WIDE>(static_cast<const T*>(a.k) + tok * a.k_stride[0] + h * a.k_stride[1] + lane * kV, k);
+    load_row<T, WIDE>(static_cast<const T*>(a.v) + tok * a.v_stride[0] + h * a.v_stride[1] + lane * kV, v);
     if (slot >= a.c.pages << a.c.log2_page) {
       if (lane == 0) report_error(a.errw, ERRW_BOUNDS);
       slot = -1;
@@ -169,7 +180,7 @@ __device__ __forceinline__ void widen(const void* src, float scale, T* dst) {
     Pack<T, P> o;
 #pragma unroll
     for (int j = 0; j < P; ++j) o.e[j] = from_f<T>(x[i + j]);
-    *reinterpret_cast<Pack<T, P>*>(dst + i) = o;
+    __stcs(reinterpret_cast<uint4*>(dst + i), *reinterpret_cast<const uint4*>(&o));  // read next by another kernel
   }
 }
 
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheIoArgs 
 
 template <typename T, int KIND, int D>
 cudaError_t write_d(const CacheIoArgs& a, cudaStream_t st) {
-  constexpr int R = kThreads / (D / 8);  // rows of a block
+  constexpr int R = kThreads / (D / kV);  // rows of a block
   const int64_t grid = (a.n * a.c.heads + R - 1) / R;
   constexpr int64_t W = 16 / sizeof(T);
   const bool wide = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0 &&
@@ -224,10 +235,8 @@ cudaError_t read_d(const CacheIoArgs& a, cudaStream_t st) {
   constexpr int V = KIND == LH_CACHE_E4M3 || KIND == LH_CACHE_INT8 ? 16 : 8;
   constexpr int R = kThreads / (D / V);  // tokens of a block
   const int64_t gx = (a.n + R - 1) / R;
-  // a thread walks the heads of its token (one page lookup); with few tokens
-  // the heads are shared out until there are four blocks an SM
-  int gy = (int)(592 / gx);
-  gy = gy < 1 ? 1 : gy > a.c.heads ? a.c.heads : gy;
+  // a thread walks some heads of its token (one page lookup)
+  const int gy = (a.c.heads + kReadHeads - 1) / kReadHeads;
   cache_read_kernel<T, KIND, D><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }

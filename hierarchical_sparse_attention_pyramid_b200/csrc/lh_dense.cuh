@@ -35,6 +35,7 @@ struct MaskView {
   const int2* cols;          // [B][N] queries of a key
   const TileSpan* row_tile;  // [B][n_tiles]
   const TileSpan* col_tile;  // [B][n_tiles]
+  const int* padded;         // [B]
   int causal;
 };
 
@@ -70,6 +71,7 @@ struct SpanBuffer {
   int4 *row_tile, *col_tile;  // [B][n_tiles]
   int2 *rows, *cols;          // [B][N]
   int* scratch;               // [B][N]
+  int* padded;                // [B] whether a row of the batch has padding
 };
 inline SpanBuffer span_buffer(void* p, int64_t B, int64_t N) {
   const int64_t tiles = B * ((N + 127) / 128);
@@ -79,10 +81,33 @@ inline SpanBuffer span_buffer(void* p, int64_t B, int64_t N) {
   s.rows = reinterpret_cast<int2*>(s.col_tile + tiles);
   s.cols = s.rows + B * N;
   s.scratch = reinterpret_cast<int*>(s.cols + B * N);
+  s.padded = s.scratch + B * N;
   return s;
 }
 inline size_t span_bytes(int64_t B, int64_t N) {
-  return (size_t)(B * ((N + 127) / 128)) * 2 * sizeof(int4) + (size_t)(B * N) * (2 * sizeof(int2) + sizeof(int));
+  return (size_t)(B * ((N + 127) / 128)) * 2 * sizeof(int4) + (size_t)(B * N) * (2 * sizeof(int2) + sizeof(int)) +
+         (size_t)B * sizeof(int);
+}
+
+// Padding tokens of a tile (nothing sees them, they see nothing): what they
+// hold is not to be used, yet a product multiplies it by zero, and zero times a
+// NaN is not zero.  So a tile with padding has those rows zeroed in shared
+// memory before such a product reads them.  Whether a tile has any its bounds
+// say, which the kernels ask only where a row of the batch has padding and a
+// tile needs masking.
+__device__ __forceinline__ bool has_padding(const MaskView& m, int b) { return m.rows && __ldg(m.padded + b) != 0; }
+__device__ __forceinline__ bool empty_keys(const MaskView& m, int b, int t, int N) {
+  return mask_col_tile(m, b, t, N).min_hi == 0;
+}
+__device__ __forceinline__ bool empty_queries(const MaskView& m, int b, int t, int N) {
+  return mask_row_tile(m, b, t, N).min_hi == 0;
+}
+// zero `regions` 128-byte pieces of row r of a tile of 64-channel regions
+__device__ __forceinline__ void zero_row(uint8_t* tile, int r, int first, int regions) {
+  for (int c = first; c < first + regions; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(tile + c * (128 * 128) + r * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // strides of a [B][H][N][d] tensor in elements (d contiguous)

@@ -64,6 +64,7 @@ DenseArgs dense_args(const lh_dense_config* c, const void* spans, const float* s
     a.mask.rows = s.rows;
     a.mask.cols = s.cols;
     a.mask.row_tile = reinterpret_cast<const TileSpan*>(s.row_tile);
+    a.mask.padded = s.padded;
     a.mask.col_tile = reinterpret_cast<const TileSpan*>(s.col_tile);
   }
   a.errw = static_cast<int*>(err);

@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     const int kv = kt * 128 + t;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int2 seen = mask_col(a.mask, b, kv, a.N);
+    const bool pads = has_padding(a.mask, b);
     const unsigned len = (unsigned)max(0, seen.y - seen.x);
     bool ok = true;
     // LSE (ct < 128) or Delta (128 <= ct < 256) of query row ct & 127 of a
@@ -301,6 +302,17 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
       tc_fence_after();
       float p[32];  // P, times the cap's derivative after P^T is stored
       const int lo = seen.x - qb;
+      const bool pad = pads && !full && empty_queries(a.mask, b, qb >> 7, a.N);
+      if (pad) {
+        // padding queries of Q_j (for dK) and dO_j (for dV): warpgroups 0, 1
+        // and 2, 3 take a half of the channels each
+        ok = __all_sync(0xffffffffu, mbar_wait(&bOload[j & 1], (j >> 1) & 1, abort_flag));
+        if (!ok) continue;
+        const int2 k = mask_row(a.mask, b, qb + t, a.N);
+        if (k.y <= k.x && (g & 1) * 64 < D)
+          zero_row(smem + (g < 2 ? Lay::oQ + (j % 3) * Lay::kTile : Lay::oO + (j & 1) * Lay::kTile), t, g & 1, 1);
+        fence_proxy_async_smem();
+      }
       {
         uint32_t sr[32];
         tmem_ld32(tl + tS + g * 32, sr);
@@ -349,6 +361,11 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         uint32_t dr[32];
         tmem_ld32(tl + tDP + g * 32, dr);
         tmem_ld_wait();
+        if (pad) {  // scores and dP of padding queries may be anything
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((unsigned)(g * 32 + e - lo) >= len) p[e] = 0.f, dr[e] = 0u;
+        }
         uint32_t dh[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -379,7 +396,8 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
           tmem_ld16(tl + tDK + g * CW, rk);
         }
         tmem_ld_wait();
-      } else {
+      }
+      if (NJ == 0 || len == 0) {  // a padding key's sums may be anything
 #pragma unroll
         for (int e = 0; e < CW; ++e) rv[e] = rk[e] = 0u;
       }
@@ -638,15 +656,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     compute_sync_q();
     float del = sDel[t] + sDel[128 + t];
-    if (NJ != 1 && g == 0 && q < a.N) a.delta[(int64_t)bh * a.N + q] = del;
-    const float lse_raw = q < a.N ? a.lse[(int64_t)bh * a.N + q] : -INFINITY;
+        const float lse_raw = q < a.N ? a.lse[(int64_t)bh * a.N + q] : -INFINITY;
     const float lse = lse_raw == -INFINITY ? INFINITY : lse_raw * kLog2e;  // no key: P = 2^-inf = 0
     const float scale_log2 = a.scale * kLog2e;
     const uint64_t c2 = f2_pack(scale_log2, scale_log2);
     const uint64_t nl2 = f2_pack(-lse, -lse);
-    uint64_t d2 = f2_pack(del, del);
     const int2 keys = mask_row(a.mask, b, q, a.N);
+    const bool pads = has_padding(a.mask, b);
     const unsigned len = (unsigned)max(0, keys.y - keys.x);
+    if (len == 0) del = 0.f;  // the padding's dO may be anything
+    if (NJ != 1 && g == 0 && q < a.N) a.delta[(int64_t)bh * a.N + q] = del;
+    uint64_t d2 = f2_pack(del, del);
     const Mod mod = MOD ? make_mod(a, h) : Mod{};
     bool ok = true;
     for (int j = 0; j < NJ; ++j) {
@@ -740,6 +760,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       tc_fence_after();
+      const bool pad = pads && !full && empty_keys(a.mask, b, k0 + j, a.N);
+      if (pad) {
+        // padding keys of K_j (for dQ): each warpgroup takes half of the row
+        const int2 s = mask_col(a.mask, b, kb + t, a.N);
+        if (s.y <= s.x && g * 64 < D) zero_row(smem + Lay::oK + (j % 3) * Lay::kTile, t, g, 1);
+        fence_proxy_async_smem();
+      }
       // dP is released as soon as it is in registers, so that the next
       // tile's dP can be computed meanwhile
       uint32_t dr[2][32];
@@ -748,6 +775,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(bDPread);
+      if (pad) {  // scores and dP of padding keys may be anything
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((unsigned)(kb + g * 64 + ch * 32 + e - keys.x) >= len) p[ch][e] = 0.f, dr[ch][e] = 0u;
+      }
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
         uint32_t dh[16];
@@ -774,7 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (NJ > 0) {
           tmem_ld32(tl + tDQ + col, r);
           tmem_ld_wait();
-        } else {
+        }
+        if (NJ == 0 || len == 0) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0u;
         }

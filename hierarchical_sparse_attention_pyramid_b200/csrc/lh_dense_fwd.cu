@@ -193,9 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = tl + x * 128, to = tl + 256 + x * D;
     const int2 keys = mask_row(a.mask, b, row, a.N);
+    const bool pads = has_padding(a.mask, b);
     const Mod mod = MOD ? make_mod(a, h) : Mod{};
     const float scale_log2 = !MOD ? a.scale * kLog2e : mod.bias ? 1.f : mod.mul;
     float m_run = -INFINITY, l_run = 0.f;
+    float s_ref = 0.f;  // the score that m_run is the exponent of
     bool ok = true;
     for (int j = j_first; j < j_end; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bS[x], (j - j_first) & 1, abort_flag));
@@ -258,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float m_new = move ? m_tile : m_run;
       const float alpha = move ? fast_exp2(m_run - m_new) : 1.f;
       const float m_ref = m_new == -INFINITY ? 0.f : m_new;  // no key of the row so far: every P is 0
+      if (move) s_ref = mx;
       // rescale the O row (the tile's previous P V completed before this S)
       if (j > j_first && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
@@ -274,14 +277,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that the maximum read last is still in registers and goes first, and
       // its P V starts while the other half's P is made
       const uint64_t c2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m_ref, -m_ref);
+      const uint64_t ns2 = f2_pack(-s_ref, -s_ref);
       uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-      auto p_chunk = [&](auto masked, uint32_t (&sv)[32], int key, uint32_t dst, uint64_t& sum) {
+      auto p_chunk = [&](auto careful, uint32_t (&sv)[32], int key, uint32_t dst, uint64_t& sum) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nm2);
+          const uint64_t s2 = f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+          // The careful form takes the difference of the scores first: in
+          // s c - m a large m is off by its rounding, 2^-24 of it.
+          const uint64_t x2 = decltype(careful)::value ? f2_mul(f2_add(s2, ns2), c2) : f2_fma(s2, c2, nm2);
           float pa, pb;
-          if constexpr (decltype(masked)::value) {
+          if constexpr (decltype(careful)::value) {
             f2_unpack(x2, pa, pb);
             pa = (unsigned)(key + e - lo) < len ? fast_exp2(pa) : 0.f;
             pb = (unsigned)(key + e + 1 - lo) < len ? fast_exp2(pb) : 0.f;
@@ -297,23 +304,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st16(dst, pk);
       };
-      auto p_pass = [&](auto masked) {
-        p_chunk(masked, r[0], 64, ts + 64, rs2[0]);
+      auto p_pass = [&](auto careful) {
+        p_chunk(careful, r[0], 64, ts + 64, rs2[0]);
         tmem_ld32(ts, r[0]);
-        p_chunk(masked, r[1], 96, ts + 80, rs2[1]);
+        p_chunk(careful, r[1], 96, ts + 80, rs2[1]);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bP[2 * x + 1]);
         tmem_ld_wait32(r[0]);
         tmem_ld32(ts + 32, r[1]);
-        p_chunk(masked, r[0], 0, ts, rs2[0]);
+        p_chunk(careful, r[0], 0, ts, rs2[0]);
         tmem_ld_wait32(r[1]);
-        p_chunk(masked, r[1], 32, ts + 16, rs2[1]);
+        p_chunk(careful, r[1], 32, ts + 16, rs2[1]);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bP[2 * x]);
       };
-      if (!MOD && !full) p_pass(std::true_type{});
+      if (pads && !full && empty_keys(a.mask, b, j, a.N)) {
+        const int i = j - j0, t = (warp & 3) * 32 + lane;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bV[i & 1], (i >> 1) & 1, abort_flag));
+        if (!ok) break;
+        const int2 q = mask_col(a.mask, b, j * 128 + t, a.N);
+        if (q.y <= q.x) zero_row(smem + Lay::oV + (i & 1) * Lay::kTile, t, 0, D / 64);
+        fence_proxy_async_smem();
+      }
+      // masked tiles, and rows whose scores are beyond 2^16 in size
+      if (!MOD && (!full || __any_sync(0xffffffffu, fabsf(m_ref) > 65536.f))) p_pass(std::true_type{});
       else p_pass(std::false_type{});
       float rsa, rsb;
       f2_unpack(f2_add(rs2[0], rs2[1]), rsa, rsb);

@@ -65,7 +65,7 @@ __device__ __forceinline__ int4 bounds_of(const Bounds& b) {
 __global__ void __launch_bounds__(kThreads)
     mask_spans_kernel(const int32_t* __restrict__ docs, const uint8_t* __restrict__ prefix, int N, int causal, int K,
                       int4* __restrict__ row_tile, int4* __restrict__ col_tile, int2* __restrict__ rows,
-                      int2* __restrict__ cols, int* scratch) {
+                      int2* __restrict__ cols, int* scratch, int* __restrict__ padded) {
   __shared__ int sInt[kWarps];
   __shared__ uint64_t sLong[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -99,10 +99,12 @@ __global__ void __launch_bounds__(kThreads)
     }
   };
   // backwards over the chunks: what follows each
+  int any_pad = 0;
   int after_edge = N, after_plain = N;  // first document start, first plain token after the chunk
   for (int c = chunks - 1; c >= 0; --c) {
     const int i0 = c * per + warp * 32 * K, own = i0 + lane * 32;
     load_masks(i0);
+    any_pad |= pads != 0;
     if (chunks > 1) {
       int* k = kept + c * (per / 32 * 3 + 2);
       if (lane < K) {
@@ -120,7 +122,8 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
-  __syncthreads();
+  any_pad = __syncthreads_or(any_pad);
+  if (threadIdx.x == 0) padded[blockIdx.x] = any_pad;
   // forwards: the spans.  carry: start of the document that a chunk begins in
   // and the end of its prefix
   uint64_t carry = 0;
@@ -194,7 +197,7 @@ cudaError_t launch_mask_spans(const int32_t* docs, const uint8_t* prefix, int64_
   int K = ((N + kThreads - 1) / kThreads + 3) / 4 * 4;
   if (K > 32) K = 32;
   mask_spans_kernel<<<dim3((unsigned)B), kThreads, 0, st>>>(docs, prefix, N, causal, K, s.row_tile, s.col_tile, s.rows,
-                                                            s.cols, s.scratch);
+                                                            s.cols, s.scratch, s.padded);
   return cudaGetLastError();
 }
 

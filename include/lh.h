@@ -510,7 +510,9 @@ lh_status lh_dense_fwd(const lh_dense_config *cfg, const void *q, const void *k,
 
 /* Its gradients (none for the slopes), dK and dV summed over the query heads
  * that share a key head; every gradient is written once, in an order that does
- * not depend on scheduling.  In: the forward's inputs, o and lse, and dout.
+ * not depend on scheduling.  Probabilities are recomputed from the fp32 LSE,
+ * whose rounding is theirs: 2^-24 |LSE| relative, which scores of up to 2^12 in
+ * size keep below the gradients' own rounding.  In: the forward's inputs, o and lse, and dout.
  * Scratch: delta [B][Hq][N] fp32 (left holding rowsum(dout * o)). */
 lh_status lh_dense_bwd(const lh_dense_config *cfg, const void *q, const void *k, const void *v, const void *o,
                        const void *dout, const float *lse, const void *spans, const float *slopes, float *delta,

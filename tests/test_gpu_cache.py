@@ -1,0 +1,315 @@
+"""The paged cache on the GPU: writing (quantised), reading back, and the
+attention of single tokens and trees over it, against plain fp64 forms."""
+
+import pytest
+import torch
+
+import hierarchical_sparse_attention_pyramid_b200 as lh
+from tests import dense_util as du
+
+pytestmark = pytest.mark.gpu
+KINDS = ["bf16", "fp16", "e4m3", "int8"]
+
+
+def randn(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).cuda()
+
+
+def paging(lens, page, seed=0, spare=2):
+    """-> page_table [seqs, width] (unused entries -1), number of pages, slots of all positions in sequence order."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    order = torch.randperm(sum(need) + spare, generator=g)
+    table = torch.full((len(lens), max(1, max(need))), -1, dtype=torch.int32)
+    at, slots = 0, []
+    for s, n in enumerate(need):
+        table[s, :n] = order[at:at + n].int()
+        at += n
+        p = torch.arange(lens[s])
+        slots.append(table[s].long()[p // page] * page + p % page)
+    return table.cuda(), sum(need) + spare, torch.cat(slots).cuda()
+
+
+def starts_of(lens):
+    return torch.tensor([0] + list(lens)).cumsum(0).int().cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,d,page,lens", [(2, 128, 16, (1, 40, 0, 17)), (3, 64, 8, (9, 8, 100)), (1, 128, 256, (300,))])
+def test_write_and_read(kind, dtype, heads, d, page, lens):
+    table, pages, slots = paging(lens, page)
+    cache = lh.KVCache.empty(pages, heads, page, d, kind)
+    n = sum(lens)
+    k, v = randn((n, heads, d), dtype, 1, 3.0), randn((n, heads, d), dtype, 2, 1e-3)
+    k[0, 0] = 0
+    lh.cache_write(cache, k, v, slots)
+    got = lh.cache_read(cache, table, starts_of(lens), n, dtype=dtype)
+    lh.check_dense_error()
+    u = du.half_step(dtype)
+    for x, y in zip((k, v), got):
+        if kind in ("bf16", "fp16"):
+            held = x.to(torch.bfloat16 if kind == "bf16" else torch.float16)
+            assert torch.equal(y, held.to(dtype))
+            continue
+        # each held value nearest, but for borders that the fp32 multiplier and scale (2^-22) may cross
+        want, step = du.quantise64(x, kind)
+        err = (y.double() - want).abs()
+        # half a step of the output: relative for its normal numbers, and half of the one step that subnormal ones
+        # have (fp16: values of this test around 1e-5 are below its 2^-14, where steps are 2^-24)
+        near = u * want.abs() + torch.finfo(dtype).smallest_normal * u + 2.0 ** -21 * want.abs() + 1e-30
+        crossed = err > near
+        assert (err <= step + near).all()
+        assert crossed.float().mean() <= 1e-3
+        # and never further from x than half a step of the held type
+        assert ((y.double() - x.double()).abs() <= step / 2 * (1 + 2.0 ** -12) + near + 2.0 ** -20 * x.abs().amax(-1, keepdim=True).double()).all()
+
+
+def test_write_takes_strides_skips_and_keeps_the_rest():
+    heads, d, page = 2, 64, 16
+    cache = lh.KVCache.empty(4, heads, page, d, "e4m3")
+    for t in (cache.k, cache.v):
+        t.view(torch.int8).fill_(17)
+    cache.k_scale.fill_(2.0)
+    cache.v_scale.fill_(3.0)
+    qkv = randn((10, 6, d), torch.bfloat16, 1)
+    k, v = qkv[:, 2:4], qkv[:, 4:6]
+    slots = torch.arange(10, device="cuda") * 5
+    slots[3] = -1
+    lh.cache_write(cache, k, v, slots)
+    want = lh.KVCache.empty(4, heads, page, d, "e4m3")
+    for t in (want.k, want.v):
+        t.view(torch.int8).fill_(17)
+    want.k_scale.fill_(2.0)
+    want.v_scale.fill_(3.0)
+    live = slots >= 0
+    lh.cache_write(want, k[live].contiguous(), v[live].contiguous(), slots[live].contiguous())
+    for a, b in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), (want.k, want.v, want.k_scale, want.v_scale)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    touched = (cache.k.view(torch.int8) != 17).any(-1).any(1).flatten().nonzero().flatten().tolist()
+    assert set(touched) <= set(slots[live].tolist())
+    # rows that 16-byte loads cannot take
+    odd = torch.empty(10 * heads * d + 1, dtype=torch.bfloat16, device="cuda")[1:].view(10, heads, d)
+    odd.copy_(k)
+    lh.cache_write(want, odd, odd, slots.clamp_min(0) + (slots < 0) * 63)
+    lh.cache_write(cache, k, k, slots.clamp_min(0) + (slots < 0) * 63)
+    assert torch.equal(cache.k.view(torch.uint8), want.k.view(torch.uint8))
+    # nothing to write
+    lh.cache_write(cache, k[:0], v[:0], slots[:0])
+
+
+def test_rows_that_are_not_finite():
+    cache = lh.KVCache.empty(1, 1, 8, 64, "int8")
+    k = torch.ones(3, 1, 64, device="cuda")
+    k[0, 0, 5], k[1, 0, 6] = float("nan"), float("inf")
+    k[2] = 1e-42  # subnormal: kept to what fp32 can scale
+    table, starts = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    lh.cache_write(cache, k, k, torch.arange(3, device="cuda"))
+    got, _ = lh.cache_read(cache, table, starts, 3, dtype=torch.float32)
+    assert got[:2].isnan().all() and got[2].isfinite().all() and (got[2] <= 1e-41).all()
+
+
+def test_read_leaves_other_rows_and_reports_bad_pages():
+    lens = (20, 5)
+    table, pages, slots = paging(lens, 8)
+    cache = lh.KVCache.empty(pages, 1, 8, 64, "bf16")
+    x = randn((25, 1, 64), torch.bfloat16, 1)
+    lh.cache_write(cache, x, -x, slots)
+    out = tuple(torch.full((40, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    starts = torch.tensor([3, 23, 28], dtype=torch.int32, device="cuda")
+    lh.cache_read(cache, table, starts, 40, out=out)
+    assert torch.equal(out[0][3:28], x) and torch.equal(out[1][3:28], -x)
+    assert (out[0][:3] == 7).all() and (out[0][28:] == 7).all()
+    lh.check_dense_error()
+    bad = table.clone()
+    bad[0, 1] = pages
+    bad[1, 0] = -5
+    lh.cache_read(cache, bad, starts, 40, out=out)
+    with pytest.raises(lh._lib.LhError, match="LH_ERR_DEVICE"):
+        lh.check_dense_error()
+    lh.check_dense_error()
+    lh.cache_write(cache, x[:1], x[:1], torch.tensor([pages * 8], device="cuda"))
+    with pytest.raises(lh._lib.LhError, match="LH_ERR_DEVICE"):
+        lh.check_dense_error()
+
+
+def filled(kind, lens, heads, d, page, seed=0, v_scale=1.0):
+    """A cache with random sequences; what it stands for, per sequence, in fp64."""
+    table, pages, slots = paging(lens, page, seed)
+    cache = lh.KVCache.empty(pages, heads, page, d, kind)
+    cache.k.view(torch.uint8).fill_(0xff)  # NaN (or -1) wherever nothing is written
+    cache.v.view(torch.uint8).fill_(0xff)
+    if cache.k_scale is not None:
+        cache.k_scale.fill_(float("nan"))
+        cache.v_scale.fill_(float("nan"))
+    n = sum(lens)
+    k, v = randn((n, heads, d), torch.float32, seed + 1), randn((n, heads, d), torch.float32, seed + 2, v_scale)
+    v *= torch.exp(randn((n, 1, 1), torch.float32, seed + 3))  # rows of different size
+    lh.cache_write(cache, k, v, slots)
+    ks, vs = (t.double() for t in lh.cache_read(cache, table, starts_of(lens), n, dtype=torch.float32))
+    cut = [0] + torch.tensor(lens).cumsum(0).tolist()
+    return cache, table, [ks[a:b] for a, b in zip(cut, cut[1:])], [vs[a:b] for a, b in zip(cut, cut[1:])]
+
+
+ATTN = [
+    # kind, dtype, G, heads, d, page, lens, tokens of each sequence, softcap, alibi, tree
+    ("bf16", torch.bfloat16, 4, 2, 128, 16, (1, 7, 16, 300), None, 0.0, 0, 0),
+    ("fp16", torch.float16, 1, 3, 64, 8, (9, 129, 0), None, 30.0, 1, 0),
+    ("e4m3", torch.bfloat16, 8, 1, 128, 64, (1000, 128, 127), None, 50.0, 0, 0),
+    ("e4m3", torch.float16, 5, 2, 64, 32, (64, 31, 33), None, 0.0, 1, 0),
+    ("int8", torch.bfloat16, 16, 1, 128, 128, (257, 1), None, 0.0, 0, 0),
+    ("int8", torch.float16, 2, 2, 64, 16, (513, 40), (3, 0), 20.0, 0, 0),
+    ("bf16", torch.bfloat16, 4, 1, 64, 16, (90, 33, 2), (5, 1, 2), 0.0, 1, 0),
+    ("e4m3", torch.bfloat16, 4, 2, 128, 16, (200, 24, 70), (24, 24, 10), 0.0, 0, 1),
+    ("fp16", torch.float16, 8, 1, 128, 32, (65, 300), (64, 13), 10.0, 0, 1),
+    ("int8", torch.bfloat16, 3, 2, 128, 4096, (4200,), (2,), 0.0, 0, 0),
+]
+
+
+def random_tree(tokens, seed):
+    g = torch.Generator().manual_seed(seed)
+    out = []
+    for T in tokens:
+        seen = []
+        for t in range(T):
+            parent = int(torch.randint(-1, t, (1,), generator=g)) if t else -1
+            seen.append((seen[parent] if parent >= 0 else 0) | (1 << t))
+        out += [m - (1 << 64) if m >= 1 << 63 else m for m in seen]
+    return torch.tensor(out, dtype=torch.int64)
+
+
+@pytest.mark.parametrize("case", ATTN, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c))
+def test_cache_attention(case):
+    kind, dtype, G, heads, d, page, lens, tokens, cap, alibi, tree = case
+    cache, table, ks, vs = filled(kind, lens, heads, d, page)
+    T = [1] * len(lens) if tokens is None else list(tokens)
+    n, Hq = sum(T), G * heads
+    q = randn((n, Hq, d), dtype, 5, 1.5)
+    slopes = torch.tensor([2.0 ** -(i % 8 + 1) for i in range(Hq)], device="cuda") if alibi else None
+    masks = random_tree(T, 3).cuda() if tree else None
+    cut = [0] + torch.tensor(T).cumsum(0).tolist()
+    opt = dict(softcap=cap, slopes=slopes, tree_mask=masks)
+    if tokens is not None:
+        opt |= dict(q_start=torch.tensor(cut, dtype=torch.int32, device="cuda"), max_tokens=max(T))
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = lh.cache_attention(cache, q, table, ln, **opt)
+    lh.check_dense_error()
+    value, bound = du.cache_attention64(q, ks, vs, cut, lens, None if masks is None else
+                                        [x & (1 << 64) - 1 for x in masks.tolist()], None, cap, slopes)
+    du.check("o", got, (value, bound))
+    assert torch.equal(got, lh.cache_attention(cache, q, table, ln, **opt))
+    # strided queries, another stream, an output given
+    wide = torch.zeros(n, Hq + 2, d, dtype=dtype, device="cuda")
+    wide[:, 1:-1] = q
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lh.cache_attention(cache, wide[:, 1:-1], table, ln, out=out, **opt)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, got)
+
+
+def test_cache_attention_long_and_many():
+    """One long sequence over all SMs, and many short ones beside it: parts that end inside others."""
+    for lens in ((20000,), tuple([3] * 200 + [9000] + [130] * 60)):
+        cache, table, ks, vs = filled("int8", lens, 2, 64, 64)
+        q = randn((len(lens), 8, 64), torch.bfloat16, 5, 1.5)
+        ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        got = lh.cache_attention(cache, q, table, ln)
+        value, bound = du.cache_attention64(q, ks, vs, list(range(len(lens) + 1)), lens)
+        du.check("o", got, (value, bound))
+
+
+def test_cache_attention_values_of_any_size():
+    """Value rows of very different size in one 8-bit cache, and tiny ones: none underflows on the way."""
+    lens = (70,)
+    for size in (1e-18, 1e12):
+        cache, table, ks, vs = filled("e4m3", lens, 1, 64, 16, v_scale=size)
+        q = randn((1, 4, 64), torch.bfloat16, 5)
+        ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        value, bound = du.cache_attention64(q, ks, vs, [0, 1], lens)
+        du.check("o", lh.cache_attention(cache, q, table, ln), (value, bound))
+
+
+def test_bad_lengths_and_pages_are_cut_and_reported():
+    lens = (40, 20)
+    cache, table, ks, vs = filled("bf16", lens, 1, 64, 8)
+    q = randn((2, 2, 64), torch.bfloat16, 5)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    good = lh.cache_attention(cache, q, table, ln)
+    lh.check_dense_error()
+    bad = table.clone()
+    bad[0, 2] = 1 << 20  # keys 16-23 of sequence 0 are not seen
+    got = lh.cache_attention(cache, q, bad, ln)
+    with pytest.raises(lh._lib.LhError, match="LH_ERR_DEVICE"):
+        lh.check_dense_error()
+    assert torch.equal(got[1], good[1])
+    keep = torch.tensor([i for i in range(40) if not 16 <= i < 24], device="cuda")
+    # 32 keys at their places: no distance bias, so that only the set matters
+    value, bound = du.cache_attention64(q[:1], [ks[0][keep]], [vs[0][keep]], [0, 1], (32,))
+    du.check("o", got[:1], (value, bound))
+    for wrong in ((1 << 30, 20), (-3, 20)):
+        lh.cache_attention(cache, q, table, torch.tensor(wrong, dtype=torch.int32, device="cuda"))
+        with pytest.raises(lh._lib.LhError, match="LH_ERR_DEVICE"):
+            lh.check_dense_error()
+    # more tokens than the call allows
+    start = torch.tensor([0, 2, 2], dtype=torch.int32, device="cuda")
+    lh.cache_attention(cache, q, table, ln, q_start=start, max_tokens=1)
+    with pytest.raises(lh._lib.LhError, match="LH_ERR_DEVICE"):
+        lh.check_dense_error()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_prompt_then_steps_as_served(kind):
+    """The operators as they are used together: a prompt's queries and keys are turned, its keys and values written,
+    and the dense attention runs on what the cache stands for; then single tokens are turned, written and attended,
+    captured in one graph that is replayed for each step.  Each step's output is the last row of the dense attention
+    over all tokens so far."""
+    heads, G, d, page, prompt, steps = 2, 4, 128, 16, 45, 6
+    total = prompt + steps
+    rope = lh.Rotary.make(d, base=5e5)
+    table, pages, slots = paging((total,), page)
+    cache = lh.KVCache.empty(pages, heads, page, d, kind)
+    q = randn((1, total, heads * G, d), torch.bfloat16, 1).transpose(1, 2)
+    k, v = (randn((1, total, heads, d), torch.bfloat16, s).transpose(1, 2) for s in (2, 3))
+    qr, kr = lh.rotary(q[:, :, :prompt], k[:, :, :prompt], rope.frequencies)
+    lh.cache_write(cache, kr[0].transpose(0, 1), v[0, :, :prompt].transpose(0, 1), slots[:prompt].contiguous())
+    kc, vc = lh.cache_read(cache, table, starts_of((prompt,)), prompt)
+    first = lh.dense_attention(qr, kc.transpose(0, 1)[None], vc.transpose(0, 1)[None])
+
+    at = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    ln, slot = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    qs, ks, vs = (torch.zeros(1, h, 1, d, dtype=torch.bfloat16, device="cuda") for h in (heads * G, heads, heads))
+
+    def step():
+        a, b = lh.rotary(qs, ks, rope.frequencies, at)
+        lh.cache_write(cache, b[0].transpose(0, 1), vs[0].transpose(0, 1), slot)
+        return lh.cache_attention(cache, a[0].transpose(0, 1), table, ln)
+
+    def feed(t):
+        at.fill_(t)
+        ln.fill_(t + 1)
+        slot.copy_(slots[t:t + 1])
+        for dst, src in ((qs, q), (ks, k), (vs, v)):
+            dst.copy_(src[:, :, t:t + 1])
+
+    feed(prompt)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for t in range(prompt, total):
+        feed(t)
+        graph.replay()
+        kc, vc = lh.cache_read(cache, table, starts_of((t + 1,)), t + 1)
+        q_all = lh.rotary(q[:, :, :t + 1], None, rope.frequencies)[0]
+        value, bound = du.cache_attention64(q_all[0, :, t][None], [kc.double()], [vc.double()], [0, 1], (t + 1,))
+        du.check("step", out, (value, bound))
+        dense = lh.dense_attention(q_all, kc.transpose(0, 1)[None], vc.transpose(0, 1)[None])
+        du.check("dense", dense[0, :, t][None], (value, bound))
+        # earlier rows see the same keys: the prompt's outputs again
+        du.check("prompt", dense[:, :, :prompt], (first.double(), 2 * du.half_step(torch.bfloat16) * (1 + first.double().abs())))
+    lh.check_dense_error()
