@@ -21,28 +21,21 @@
 // relative to a power of two above the scales met so far.  The scale of a key
 // enters its score.
 //
-// The work is a list of units of 128 keys: sequence by sequence, for each of
-// its heads and tiles of 8 to 32 query rows all the keys.  As many blocks of 4
-// warps as the GPU holds at once take equal stretches of that list, whatever
-// the lengths of the sequences are; a stretch may end inside one (sequence,
-// head, row tile) and begin inside another.  The warps' running maxima, sums
-// and outputs are joined in shared memory in warp order; what a block has of
-// an unfinished one goes to one of its two places in the workspace, and a
-// second kernel joins those in block order, so that results do not depend on
-// scheduling.
+// A block of 4 warps takes its stretch of the work list (lh_cache_attn.cuh)
+// for 8 or 16 query rows of a head; the warps' running maxima, sums and
+// outputs are joined in shared memory in warp order.
 #include <cuda_fp16.h>
 #include <math.h>
 
 #include <type_traits>
 
-#include "lh_cache.cuh"
-#include "lh_dense.cuh"
+#include "lh_cache_attn.cuh"
 
 namespace lh {
 namespace {
 
 // query rows (tokens x heads of a group) that a block takes of `rows`
-int cache_attn_row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int cache_attn_row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 template <bool F16>
@@ -59,51 +52,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// two e4m3 bytes (the low half of y) as fp16
-__device__ __forceinline__ uint32_t e4m3_half2(uint32_t y) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(y));
-  return r;
-}
-// bytes i and j of y, int8 values raised by 128, as fp16: the bits of 1024 + u
-// less 1152
-__device__ __forceinline__ uint32_t u8_half2(uint32_t y, int i, int j) {
-  const uint32_t u = __byte_perm(y, 0x64646464u, (uint32_t)(i | 4 << 4 | j << 8 | 4 << 12));
-  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), off);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// the four values of a word of one row: (0, 1), (2, 3)
-template <int KIND>
-__device__ __forceinline__ void widen_row(uint32_t w, uint32_t& b0, uint32_t& b1) {
-  if constexpr (KIND == LH_CACHE_E4M3) {
-    b0 = e4m3_half2(w);
-    b1 = e4m3_half2(w >> 16);
-  } else {
-    w ^= 0x80808080u;
-    b0 = u8_half2(w, 0, 1);
-    b1 = u8_half2(w, 2, 3);
-  }
-}
-// the four columns of a word of two rows: b[i] = (x_i, z_i)
-template <int KIND>
-__device__ __forceinline__ void widen_cols(uint32_t x, uint32_t z, uint32_t (&b)[4]) {
-  uint32_t lo = __byte_perm(x, z, 0x5140), hi = __byte_perm(x, z, 0x7362);
-  if constexpr (KIND == LH_CACHE_E4M3) {
-    b[0] = e4m3_half2(lo);
-    b[1] = e4m3_half2(lo >> 16);
-    b[2] = e4m3_half2(hi);
-    b[3] = e4m3_half2(hi >> 16);
-  } else {
-    lo ^= 0x80808080u;
-    hi ^= 0x80808080u;
-    b[0] = u8_half2(lo, 0, 1);
-    b[1] = u8_half2(lo, 2, 3);
-    b[2] = u8_half2(hi, 0, 1);
-    b[3] = u8_half2(hi, 2, 3);
-  }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {  // zeros where not live
@@ -143,63 +91,15 @@ struct Shape {
   static constexpr int kStage = 2 * kTile + (kHeld8 ? 2 * kKeys * 4 : 0);
   static constexpr int kStages = kTile >= 4096 ? 2 : 4;   // 16 KB a warp
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr bool kQShared = NB > 2;                // query fragments in shared memory instead of registers
-  static constexpr int kQ = kQShared ? NB * (D / 16) * 256 : 0;
   static constexpr int kOutRow = D + 4;                   // floats of a row of the warps' results
   static constexpr int kOut = kWarps * NB * 8 * (kOutRow + 2) * 4;  // over the ring
-  static constexpr int kSmem = kQ + (kRing > kOut ? kRing : kOut);
+  static constexpr int kSmem = kRing > kOut ? kRing : kOut;
 };
-
-constexpr int kUnit = kWarps * 32;  // keys of a unit of work
-// Units that a (sequence, head, row tile) counts before its keys, for what a
-// block spends to begin and end one (measured: about what two units of keys
-// cost); they come first and hold no keys.
-constexpr int kBegin = 2;
-
-// tokens of a sequence, cut to what the call allows (an error is reported
-// once, by `report`)
-struct Seq {
-  int tok0, T, len;
-};
-__device__ __forceinline__ Seq load_seq(const CacheAttnArgs& a, int s, bool report) {
-  Seq q{s, 1, __ldg(a.lens + s)};
-  if (a.q_start) {
-    q.tok0 = __ldg(a.q_start + s);
-    q.T = __ldg(a.q_start + s + 1) - q.tok0;
-  }
-  const int most = a.width << a.c.log2_page;
-  if (q.T < 0 || q.T > a.max_tokens || q.tok0 < 0 || q.tok0 + (int64_t)q.T > a.n_tok || q.len < 0 || q.len > most) {
-    if (report) report_error(a.errw, ERRW_BOUNDS);
-    q.T = max(0, min(q.T, a.max_tokens));
-    if (q.tok0 < 0 || q.tok0 + (int64_t)q.T > a.n_tok) q.T = 0;
-    q.len = max(0, min(q.len, most));
-  }
-  return q;
-}
-__device__ __forceinline__ int key_units(int len) { return kBegin + max(1, (len + kUnit - 1) / kUnit); }
-// units of a sequence: heads x row tiles x units of each
-__device__ __forceinline__ int64_t seq_units(const CacheAttnArgs& a, const Seq& q, int rows_per_tile) {
-  const int tiles = (q.T * (a.Hq / a.c.heads) + rows_per_tile - 1) / rows_per_tile;
-  return (int64_t)a.c.heads * tiles * key_units(q.len);
-}
-// sum over the block of a value per thread (N warps); scratch: N + 1 int64
-template <int N>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t t = 0;
-#pragma unroll
-  for (int w = 0; w < N; ++w) t += scratch[w];
-  __syncthreads();
-  return t;
-}
 
 // NB: tiles of 8 query rows that a block takes (each conversion of a held
 // value then serves NB matrix instructions)
 template <int D, int KIND, bool F16, int NB>
-__global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 3)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
   using Sh = Shape<D, KIND, NB>;
   constexpr bool HELD8 = Sh::kHeld8, HALF = F16 || HELD8;  // HALF: fp16 matrix operands
@@ -210,98 +110,31 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
   constexpr int VE = VB / BYTES, VC = D / (8 * VE), VW = VB / 4;
   constexpr float kPUp = HELD8 ? 64.f : 1.f;  // raises probabilities (at most 2^8) within fp16's range
   extern __shared__ __align__(128) uint8_t smem[];
-  uint2* sQ = reinterpret_cast<uint2*>(smem);                           // [NB][STEPS][32] where shared
-  float* sO = reinterpret_cast<float*>(smem + Sh::kQ);                  // later [kWarps][NB * 8][kOutRow]
+  float* sO = reinterpret_cast<float*>(smem);                           // later [kWarps][NB * 8][kOutRow]
   float* sML = sO + kWarps * NB * 8 * Sh::kOutRow;                      // [kWarps][NB * 8][2]
 
-  __shared__ int64_t sScan[kWarps + 2];
-  __shared__ int sSeq;
+  __shared__ int64_t scan[kWarps + 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = a.Hq / a.c.heads;
-  // ------------------------------------------------------------ the block's stretch of the work
-  // a thread sums the units of a run of sequences; the one whose run holds the
-  // stretch's first unit looks for its sequence
-  int64_t u, u_end;
-  int s;
-  int64_t in_seq;  // u within its sequence
-  {
-    const int per = (a.seqs + kThreads - 1) / kThreads;
-    const int s0 = min(a.seqs, (int)threadIdx.x * per), s1 = min(a.seqs, s0 + per);
-    int64_t mine = 0;
-    for (int i = s0; i < s1; ++i) mine += seq_units(a, load_seq(a, i, blockIdx.x == 0), 8 * NB);
-    int64_t incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += y;
-    }
-    if (lane == 31) sScan[warp] = incl;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sScan[w];
-      total += sScan[w];
-    }
-    before += incl - mine;
-    const int64_t blocks = min((int64_t)gridDim.x, total);  // no block has an empty stretch
-    if (blockIdx.x >= blocks) return;
-    u = total * blockIdx.x / blocks;
-    u_end = total * (blockIdx.x + 1) / blocks;
-    __syncthreads();
-    if (u >= before && u < before + mine) {
-      int i = s0;
-      int64_t at = u - before;
-      for (;;) {
-        const int64_t n = seq_units(a, load_seq(a, i, false), 8 * NB);
-        if (at < n) break;
-        at -= n;
-        ++i;
-      }
-      sSeq = i;
-      sScan[0] = at;
-    }
-    __syncthreads();
-    s = sSeq;
-    in_seq = sScan[0];
-  }
-  Seq seq = load_seq(a, s, false);
+  cudaTriggerProgrammaticLaunchCompletion();  // the join may take its place beside this (it waits for the results)
+  Stretch stretch = find_stretch<kWarps>(a, 8 * NB, scan);
+  if (stretch.u >= stretch.u_end) return;
+  Seq seq = load_seq(a, stretch.s, false);
+  Piece piece;
 
-  while (u < u_end) {
-    // ------------------------------------------------------------ one (sequence, head, row tile), all or some of its keys
-    const int kt_n = key_units(seq.len);
-    const int row_tiles = (seq.T * G + 8 * NB - 1) / (8 * NB);
-    if (in_seq >= (int64_t)a.c.heads * row_tiles * kt_n) {  // the next sequence with units
-      in_seq = 0;
-      seq = load_seq(a, ++s, false);
-      continue;
-    }
-    const int inst = (int)(in_seq / kt_n), from = (int)(in_seq % kt_n);
-    const int to = (int)min((int64_t)kt_n, from + (u_end - u));
-    u += to - from;
-    in_seq += to - from;
-    if (to <= kBegin) continue;  // no keys
-    const int kt0 = max(from - kBegin, 0), kt1 = to - kBegin;
-    const int hk = inst / row_tiles, rt = inst % row_tiles;
-    const int tok0 = seq.tok0, len = seq.len;
-    const int r0 = rt * 8 * NB, n_rows = seq.T * G;  // row r: token r / G, head r % G of the group
-    const int k0 = kt0 * kUnit, k1 = min(len, kt1 * kUnit);
-    const int ctx = len - seq.T;        // keys before the query tokens' own
+  while (next_piece(a, 8 * NB, stretch, seq, piece)) {
+    const int s = stretch.s, hk = piece.hk, tok0 = seq.tok0, len = seq.len, k0 = piece.k0, k1 = piece.k1;
+    const int r0 = piece.rt * 8 * NB, n_rows = seq.T * G;  // row r: token r / G, head r % G of the group
+    const int ctx = len - seq.T;                           // keys before the query tokens' own
 
     // ------------------------------------------------------------ the ring of keys
-    const int page_mask = (1 << a.c.log2_page) - 1;
     const int32_t* table = a.table + (int64_t)s * a.width;
     constexpr uint32_t kNone = 0xffffffffu;
-    // lane j looks up the 8 keys from key + 8 j on (pages hold 8 tokens or
-    // more): their first row among the cache's rows, kNone for none
+    // lane j looks up the 8 keys from key + 8 j on (pages hold 8 tokens or more)
     auto look_up = [&](int key) -> uint32_t {
       const int kk = key + 8 * lane;
-      if (lane >= NT || kk >= k1) return kNone;
-      const int p = __ldg(table + (kk >> a.c.log2_page));
-      if (p >= 0 && p < a.c.pages) return (((uint32_t)p * a.c.heads + hk) << a.c.log2_page) + (kk & page_mask);
-      report_error(a.errw, ERRW_BOUNDS);
-      return kNone;
+      return lane >= NT || kk >= k1 ? kNone : key_rows(a, table, hk, kk);
     };
     const uint32_t ring = sm100::smem_u32(sO) + warp * (STAGES * Sh::kStage);
     // 16-byte units of a row are permuted by the row, so that the lanes of one
@@ -399,25 +232,14 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
     const float pre = cap ? a.scale / a.softcap : a.scale * kLog2e, cap2 = a.softcap * kLog2e;
     // this thread's columns of a tile: query rows nb * 8 + 2t, 2t + 1
     float qf[NB][2];  // factor of the row's scores
-    uint2 qr[Sh::kQShared ? 1 : NB][STEPS];
-    static_assert(NB <= kWarps, "a warp a tile");
+    uint2 qr[NB][STEPS];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       float up;
-      if constexpr (Sh::kQShared) {
-        uint2 f[STEPS];
-        load_q(nb, f, up);  // every warp needs the factors; one of them leaves the fragments
-        if (warp == nb) {
-#pragma unroll
-          for (int i = 0; i < STEPS; ++i) sQ[(nb * STEPS + i) * 32 + lane] = f[i];
-        }
-      } else {
-        load_q(nb, qr[nb], up);
-      }
+      load_q(nb, qr[nb], up);
       qf[nb][0] = pre / __shfl_sync(0xffffffffu, up, 8 * t);
       qf[nb][1] = pre / __shfl_sync(0xffffffffu, up, 8 * t + 4);
     }
-    if constexpr (Sh::kQShared) __syncthreads();
 
     constexpr int MI = VC * VE / 2;  // accumulators of a tile: 16 output channels each
     float acc[NB][MI][4];
@@ -474,8 +296,7 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
             }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              const uint2 qb = Sh::kQShared ? sQ[(nb * STEPS + st) * 32 + lane] : qr[Sh::kQShared ? 0 : nb][st];
-              mma<HALF>(NB == 1 && (st & 1) ? s2[NB == 1 ? k2 : 0] : sc[nb][k2], ka, qb.x, qb.y);
+              mma<HALF>(NB == 1 && (st & 1) ? s2[NB == 1 ? k2 : 0] : sc[nb][k2], ka, qr[nb][st].x, qr[nb][st].y);
             }
           }
         }
@@ -679,32 +500,33 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
         o[2] = fmaf(f, u.z, o[2]);
         o[3] = fmaf(f, u.w, o[3]);
       }
-      if (kt0 == 0 && to == kt_n) {
+      if (piece.whole) {
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int64_t out = (int64_t)(tok0 + rr / G) * a.Hq + hk * G + rr % G;
         reinterpret_cast<uint2*>(a.o)[(out * D + ch) / 4] =
             make_uint2(pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv));
       } else {
         // place 0: a block's first piece, which another one began; place 1: its last, which it begins
-        const int64_t at = ((int64_t)blockIdx.x * 2 + (kt0 == 0)) * (8 * NB) + r;
+        const int64_t at = ((int64_t)blockIdx.x * 2 + piece.begun) * (8 * NB) + r;
         *reinterpret_cast<float4*>(a.part_o + at * D + ch) = make_float4(o[0], o[1], o[2], o[3]);
         if (ch == 0) a.part_ml[at] = make_float2(mm, sum);
       }
     }
-    __syncthreads();  // the next piece's ring and query fragments
+    __syncthreads();  // the next piece's ring
   }
 }
 
-// Joins the pieces of every query row that lie in several blocks: a block a
-// row, its warps share the pieces out and are joined in warp order.
+// Joins the pieces of every query row that lie in several blocks.  W warps
+// take a row (8 where a row has many pieces, else one, and a block 8 rows):
+// they share its pieces out and are joined in warp order.
 constexpr int kJoinWarps = 8;
-template <int D, bool F16>
+template <int D, bool F16, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a, int rows_per_tile, int blocks) {
-  __shared__ float sO[kJoinWarps][D];
+  __shared__ float sO[W == 1 ? 1 : W][D];
   __shared__ float sL[kJoinWarps], sM[kJoinWarps];
-  __shared__ int64_t scratch[kJoinWarps];
-  const int64_t out = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t out = W == 1 ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x;
   const int tok = (int)(out / a.Hq), head = (int)(out % a.Hq), G = a.Hq / a.c.heads;
   int s = tok;
   if (a.q_start) {
@@ -717,14 +539,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     s = lo;
   }
   const Seq seq = s < a.seqs ? load_seq(a, s, false) : Seq{0, 0, 0};
+  // units before the sequence, and of all (every warp adds them up)
   int64_t before = 0, all = 0;
-  for (int i = threadIdx.x; i < a.seqs; i += kJoinWarps * 32) {
+  for (int i = lane; i < a.seqs; i += 32) {
     const int64_t n = seq_units(a, load_seq(a, i, false), rows_per_tile);
     all += n;
     if (i < s) before += n;
   }
-  all = block_sum<kJoinWarps>(all, scratch);
-  before = block_sum<kJoinWarps>(before, scratch);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+  }
   const int r = (tok - seq.tok0) * G + head % G, kt_n = key_units(seq.len);
   const int row_tiles = (seq.T * G + rows_per_tile - 1) / rows_per_tile;
   const int64_t end = before + (int64_t)(head / G * row_tiles + r / rows_per_tile + 1) * kt_n;
@@ -732,25 +558,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int64_t nb = min((int64_t)blocks, all);
   auto block_of = [&](int64_t u) { return (int)(((u + 1) * nb + all - 1) / all - 1); };
   // a token of no sequence is left as it is
-  const bool live = tok >= seq.tok0 && tok < seq.tok0 + seq.T;
+  const bool live = out < a.n_tok * a.Hq && tok >= seq.tok0 && tok < seq.tok0 + seq.T;
   const int c0 = live ? block_of(end - kt_n + kBegin) : 0, c1 = live ? block_of(end - 1) : 0;
   cudaGridDependencySynchronize();  // every block: what follows in the stream waits for this kernel alone
-  if (c0 == c1) return;  // written by that block
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (c0 == c1) return;  // written by that block (W > 1: the whole block's row)
   auto place = [&](int c) { return ((int64_t)c * 2 + (c == c0)) * rows_per_tile + r % rows_per_tile; };
   float mm = -INFINITY;
-  for (int c = c0 + threadIdx.x; c <= c1; c += kJoinWarps * 32) mm = fmaxf(mm, a.part_ml[place(c)].x);
+  for (int c = c0 + (W == 1 ? lane : (int)threadIdx.x); c <= c1; c += W * 32) mm = fmaxf(mm, a.part_ml[place(c)].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-  if (lane == 0) sM[warp] = mm;
-  __syncthreads();
+  if constexpr (W > 1) {
+    if (lane == 0) sM[warp] = mm;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, sM[w]);
+    for (int w = 0; w < W; ++w) mm = fmaxf(mm, sM[w]);
+  }
   const float ref = mm == -INFINITY ? 0.f : mm;
   constexpr int C = D / 32;
   float o[C] = {}, sum = 0.f;
 #pragma unroll 8
-  for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+  for (int c = c0 + (W == 1 ? 0 : warp); c <= c1; c += W) {
     const float2 x = a.part_ml[place(c)];
     const float f = sm100::fast_exp2(x.x - ref);
     sum = fmaf(f, x.y, sum);
@@ -758,21 +585,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll
     for (int i = 0; i < C; ++i) o[i] = fmaf(f, po[i], o[i]);
   }
+  if constexpr (W > 1) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) sO[warp][lane * C + i] = o[i];
-  if (lane == 0) sL[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    float total = 0.f, y[2] = {0.f, 0.f};
+    for (int i = 0; i < C; ++i) sO[warp][lane * C + i] = o[i];
+    if (lane == 0) sL[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+    sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      total += sL[w];
-      y[0] += sO[w][2 * threadIdx.x];
-      y[1] += sO[w][2 * threadIdx.x + 1];
+    for (int i = 0; i < C; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      sum += sL[w];
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] += sO[w][lane * C + i];
     }
-    const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
-    reinterpret_cast<uint32_t*>(a.o)[out * (D / 2) + threadIdx.x] = pack2<F16>(y[0] * inv, y[1] * inv);
   }
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o) + (out * D + lane * C) / 2;
+#pragma unroll
+  for (int i = 0; i < C; i += 2) dst[i / 2] = pack2<F16>(o[i] * inv, o[i + 1] * inv);
 }
 
 template <int D, int KIND, bool F16, int NB>
@@ -782,11 +614,31 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   fn<<<dim3((unsigned)a.blocks), kThreads, smem, st>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !a.part_o) return e;
-  // the join may be brought up while the pieces run; it waits for them itself
+  return cudaGetLastError();
+}
+
+template <int D, int KIND, bool F16>
+cudaError_t by_rows(const CacheAttnArgs& a, int tile, cudaStream_t st) {
+  return tile == 8 ? launch<D, KIND, F16, 1>(a, st) : launch<D, KIND, F16, 2>(a, st);
+}
+template <int D, bool F16>
+cudaError_t by_kind(const CacheAttnArgs& a, int tile, cudaStream_t st) {
+  switch (a.c.kind) {
+    case LH_CACHE_E4M3: return by_rows<D, LH_CACHE_E4M3, F16>(a, tile, st);
+    case LH_CACHE_INT8: return by_rows<D, LH_CACHE_INT8, F16>(a, tile, st);
+    default: return by_rows<D, F16 ? LH_CACHE_FP16 : LH_CACHE_BF16, F16>(a, tile, st);
+  }
+}
+
+template <int D, bool F16>
+cudaError_t join(const CacheAttnArgs& a, int rows_per_tile, cudaStream_t st) {
+  const int64_t rows = a.n_tok * a.Hq;
+  const int64_t tiles = (int64_t)a.seqs * a.c.heads *
+                        (((int64_t)a.max_tokens * (a.Hq / a.c.heads) + rows_per_tile - 1) / rows_per_tile);
+  const bool many = a.blocks >= 8 * tiles;  // pieces of a row
+  // it may be brought up while the pieces run; it waits for them itself
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.n_tok * a.Hq));
+  cfg.gridDim = dim3((unsigned)(many ? rows : (rows + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -794,44 +646,37 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16>, a, 8 * NB, a.blocks);
-}
-
-template <int D, int KIND, bool F16>
-cudaError_t by_rows(const CacheAttnArgs& a, cudaStream_t st) {
-  switch (cache_attn_row_tile((int64_t)a.max_tokens * (a.Hq / a.c.heads))) {
-    case 8: return launch<D, KIND, F16, 1>(a, st);
-    case 16: return launch<D, KIND, F16, 2>(a, st);
-    default: return launch<D, KIND, F16, 4>(a, st);
-  }
-}
-template <int D, bool F16>
-cudaError_t by_kind(const CacheAttnArgs& a, cudaStream_t st) {
-  switch (a.c.kind) {
-    case LH_CACHE_E4M3: return by_rows<D, LH_CACHE_E4M3, F16>(a, st);
-    case LH_CACHE_INT8: return by_rows<D, LH_CACHE_INT8, F16>(a, st);
-    default: return by_rows<D, F16 ? LH_CACHE_FP16 : LH_CACHE_BF16, F16>(a, st);
-  }
+  return many ? cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 8>, a, rows_per_tile, a.blocks)
+              : cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 1>, a, rows_per_tile, a.blocks);
 }
 
 }  // namespace
 
 // Blocks of a call and the rows of their places in the workspace: as many
-// blocks as 148 SMs hold at once (three each, two with 32 query rows: their
-// registers), and no more than the units that sequences as long as the table
-// would have.  No sequence has more than one unit of keys: no places.
+// blocks as 148 SMs hold at once (three each, one with tiles of 128 rows), and
+// no more than the units that sequences as long as the table would have.  No
+// sequence has more than one unit of keys: no places.
 void cache_attn_plan(int64_t seqs, int64_t kv_heads, int64_t rows, int64_t longest, int64_t* blocks, int64_t* places) {
   const int64_t tile = cache_attn_row_tile(rows);
   const int64_t keys = (longest + kUnit - 1) / kUnit;
   const int64_t inst = seqs * kv_heads * ((rows + tile - 1) / tile);
-  const int64_t fit = 148 * (tile == 32 ? 2 : 3);
+  const int64_t fit = 148 * (tile == 128 ? 1 : 3);
   *blocks = inst > fit / keys ? fit : inst * keys;
   *places = keys > 1 ? *blocks * 2 * tile : 0;
 }
 
+cudaError_t launch_cache_join(const CacheAttnArgs& a, int dtype, int rows_per_tile, cudaStream_t st) {
+  if (dtype == LH_FP16) return a.c.d == 128 ? join<128, true>(a, rows_per_tile, st) : join<64, true>(a, rows_per_tile, st);
+  return a.c.d == 128 ? join<128, false>(a, rows_per_tile, st) : join<64, false>(a, rows_per_tile, st);
+}
+
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == LH_FP16) return a.c.d == 128 ? by_kind<128, true>(a, st) : by_kind<64, true>(a, st);
-  return a.c.d == 128 ? by_kind<128, false>(a, st) : by_kind<64, false>(a, st);
+  const int tile = cache_attn_row_tile((int64_t)a.max_tokens * (a.Hq / a.c.heads));
+  cudaError_t e;
+  if (tile == 128) e = launch_cache_attn_rows(a, dtype, st);
+  else if (dtype == LH_FP16) e = a.c.d == 128 ? by_kind<128, true>(a, tile, st) : by_kind<64, true>(a, tile, st);
+  else e = a.c.d == 128 ? by_kind<128, false>(a, tile, st) : by_kind<64, false>(a, tile, st);
+  return e == cudaSuccess && a.part_o ? launch_cache_join(a, dtype, tile, st) : e;
 }
 
 }  // namespace lh
