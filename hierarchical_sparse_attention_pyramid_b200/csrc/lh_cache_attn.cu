@@ -117,7 +117,6 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = a.Hq / a.c.heads;
-  cudaTriggerProgrammaticLaunchCompletion();  // the join may take its place beside this (it waits for the results)
   Stretch stretch = find_stretch<kWarps>(a, 8 * NB, scan);
   if (stretch.u >= stretch.u_end) return;
   Seq seq = load_seq(a, stretch.s, false);

@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.c.heads;
-  cudaTriggerProgrammaticLaunchCompletion();  // the join may take its place beside this (it waits for the results)
   Stretch stretch = find_stretch<kWarps>(a, kRows, scan);
   if (stretch.u >= stretch.u_end) return;
   Seq seq = load_seq(a, stretch.s, false);
