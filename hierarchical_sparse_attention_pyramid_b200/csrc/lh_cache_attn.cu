@@ -22,7 +22,7 @@
 // enters its score.
 //
 // A block of 4 warps takes its stretch of the work list (lh_cache_attn.cuh)
-// for 8 or 16 query rows of a head; the warps' running maxima, sums and
+// for 8, 16 or 32 query rows of a head; the warps' running maxima, sums and
 // outputs are joined in shared memory in warp order.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -34,8 +34,11 @@
 namespace lh {
 namespace {
 
-// query rows (tokens x heads of a group) that a block takes of `rows`
-int cache_attn_row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
+// Query rows (tokens x heads of a group) that a block takes.  Up to 32 the
+// kernel of this file, above the tensor core tiles: one sequence of 64K e4m3
+// tokens, 4 key heads: 32 rows 39 us here and 57 there, 96 rows (three tiles of
+// 32 here) 78 and 61.
+int cache_attn_row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128; }
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 template <bool F16>
@@ -91,15 +94,17 @@ struct Shape {
   static constexpr int kStage = 2 * kTile + (kHeld8 ? 2 * kKeys * 4 : 0);
   static constexpr int kStages = kTile >= 4096 ? 2 : 4;   // 16 KB a warp
   static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr bool kQShared = NB > 2;                // query fragments in shared memory instead of registers
+  static constexpr int kQ = kQShared ? NB * (D / 16) * 256 : 0;
   static constexpr int kOutRow = D + 4;                   // floats of a row of the warps' results
   static constexpr int kOut = kWarps * NB * 8 * (kOutRow + 2) * 4;  // over the ring
-  static constexpr int kSmem = kRing > kOut ? kRing : kOut;
+  static constexpr int kSmem = kQ + (kRing > kOut ? kRing : kOut);
 };
 
 // NB: tiles of 8 query rows that a block takes (each conversion of a held
 // value then serves NB matrix instructions)
 template <int D, int KIND, bool F16, int NB>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
   using Sh = Shape<D, KIND, NB>;
   constexpr bool HELD8 = Sh::kHeld8, HALF = F16 || HELD8;  // HALF: fp16 matrix operands
@@ -110,7 +115,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   constexpr int VE = VB / BYTES, VC = D / (8 * VE), VW = VB / 4;
   constexpr float kPUp = HELD8 ? 64.f : 1.f;  // raises probabilities (at most 2^8) within fp16's range
   extern __shared__ __align__(128) uint8_t smem[];
-  float* sO = reinterpret_cast<float*>(smem);                           // later [kWarps][NB * 8][kOutRow]
+  uint2* sQ = reinterpret_cast<uint2*>(smem);                           // [NB][STEPS][32] where shared
+  float* sO = reinterpret_cast<float*>(smem + Sh::kQ);                  // later [kWarps][NB * 8][kOutRow]
   float* sML = sO + kWarps * NB * 8 * Sh::kOutRow;                      // [kWarps][NB * 8][2]
 
   __shared__ int64_t scan[kWarps + 1];
@@ -231,14 +237,25 @@ __global__ void __launch_bounds__(kThreads, 3)
     const float pre = cap ? a.scale / a.softcap : a.scale * kLog2e, cap2 = a.softcap * kLog2e;
     // this thread's columns of a tile: query rows nb * 8 + 2t, 2t + 1
     float qf[NB][2];  // factor of the row's scores
-    uint2 qr[NB][STEPS];
+    uint2 qr[Sh::kQShared ? 1 : NB][STEPS];
+    static_assert(NB <= kWarps, "a warp a tile");
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       float up;
-      load_q(nb, qr[nb], up);
+      if constexpr (Sh::kQShared) {
+        uint2 f[STEPS];
+        load_q(nb, f, up);  // every warp needs the factors; one of them leaves the fragments
+        if (warp == nb) {
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) sQ[(nb * STEPS + i) * 32 + lane] = f[i];
+        }
+      } else {
+        load_q(nb, qr[nb], up);
+      }
       qf[nb][0] = pre / __shfl_sync(0xffffffffu, up, 8 * t);
       qf[nb][1] = pre / __shfl_sync(0xffffffffu, up, 8 * t + 4);
     }
+    if constexpr (Sh::kQShared) __syncthreads();
 
     constexpr int MI = VC * VE / 2;  // accumulators of a tile: 16 output channels each
     float acc[NB][MI][4];
@@ -295,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 3)
             }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              mma<HALF>(NB == 1 && (st & 1) ? s2[NB == 1 ? k2 : 0] : sc[nb][k2], ka, qr[nb][st].x, qr[nb][st].y);
+              const uint2 qb = Sh::kQShared ? sQ[(nb * STEPS + st) * 32 + lane] : qr[Sh::kQShared ? 0 : nb][st];
+              mma<HALF>(NB == 1 && (st & 1) ? s2[NB == 1 ? k2 : 0] : sc[nb][k2], ka, qb.x, qb.y);
             }
           }
         }
@@ -511,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (ch == 0) a.part_ml[at] = make_float2(mm, sum);
       }
     }
-    __syncthreads();  // the next piece's ring
+    __syncthreads();  // the next piece's ring and query fragments
   }
 }
 
@@ -618,7 +636,11 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
 
 template <int D, int KIND, bool F16>
 cudaError_t by_rows(const CacheAttnArgs& a, int tile, cudaStream_t st) {
-  return tile == 8 ? launch<D, KIND, F16, 1>(a, st) : launch<D, KIND, F16, 2>(a, st);
+  switch (tile) {
+    case 8: return launch<D, KIND, F16, 1>(a, st);
+    case 16: return launch<D, KIND, F16, 2>(a, st);
+    default: return launch<D, KIND, F16, 4>(a, st);
+  }
 }
 template <int D, bool F16>
 cudaError_t by_kind(const CacheAttnArgs& a, int tile, cudaStream_t st) {
@@ -652,14 +674,14 @@ cudaError_t join(const CacheAttnArgs& a, int rows_per_tile, cudaStream_t st) {
 }  // namespace
 
 // Blocks of a call and the rows of their places in the workspace: as many
-// blocks as 148 SMs hold at once (three each, one with tiles of 128 rows), and
-// no more than the units that sequences as long as the table would have.  No
+// blocks as 148 SMs hold at once (three each, two with tiles of 32 rows, one
+// with tiles of 128), and no more than the units that sequences as long as the table would have.  No
 // sequence has more than one unit of keys: no places.
 void cache_attn_plan(int64_t seqs, int64_t kv_heads, int64_t rows, int64_t longest, int64_t* blocks, int64_t* places) {
   const int64_t tile = cache_attn_row_tile(rows);
   const int64_t keys = (longest + kUnit - 1) / kUnit;
   const int64_t inst = seqs * kv_heads * ((rows + tile - 1) / tile);
-  const int64_t fit = 148 * (tile == 128 ? 1 : 3);
+  const int64_t fit = 148 * (tile == 128 ? 1 : tile == 32 ? 2 : 3);
   *blocks = inst > fit / keys ? fit : inst * keys;
   *places = keys > 1 ? *blocks * 2 * tile : 0;
 }

@@ -190,7 +190,7 @@ __device__ __forceinline__ void widen_cols(uint32_t x, uint32_t z, uint32_t (&b)
 
 // launch of the join of the pieces of a call's rows (lh_cache_attn.cu)
 cudaError_t launch_cache_join(const CacheAttnArgs& a, int dtype, int rows_per_tile, cudaStream_t st);
-// more than 16 query rows of a key head: tiles of 128 on the tensor cores
+// more than 32 query rows of a key head: tiles of 128 on the tensor cores
 // (lh_cache_attn_rows.cu)
 cudaError_t launch_cache_attn_rows(const CacheAttnArgs& a, int dtype, cudaStream_t st);
 

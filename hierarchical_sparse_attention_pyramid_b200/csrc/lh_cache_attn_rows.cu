@@ -1,11 +1,15 @@
-// Attention over the paged cache for more than 16 query rows of a key head (a
+// Attention over the paged cache for more than 32 query rows of a key head (a
 // tree of drafted tokens, several heads a group): tiles of up to 128 rows on
 // the tcgen05 tensor cores.
 //
 // Each key is read and, where the cache holds 8 bits, turned into a 16-bit
-// operand once for all 128 rows.  Bound, at 128 rows and 128 channels, by the
-// softmax (one row a thread) and the conversion beside 1024 clocks of matrix
-// products a tile of 128 keys; reading the keys takes less.
+// operand once for all 128 rows.  A unit of 128 keys takes 1024 clocks of matrix
+// products at 128 channels but about 6000 in all (3.3 us; one sequence of 256K
+// e4m3 tokens, 4 key heads, 96 rows: 188 us against a floor of 42): its two
+// stages of K and V go round a chain of latencies, from the conversion over the
+// scores and the softmax of a thread a row to the product that frees them.  Two
+// groups of softmax warps, of converters, or of both (96 registers a thread),
+// and K and V freed apart did not shorten it for 8-bit caches.
 //   warps 0-3   softmax: thread t owns row t (TMEM lane t) and all 128 keys of
 //               a unit; they write the Q tile at the start of a piece and the
 //               outputs at its end

@@ -164,9 +164,11 @@ ATTN = [
     ("e4m3", torch.bfloat16, 4, 2, 128, 16, (200, 24, 70), (24, 24, 10), 0.0, 0, 1),
     ("fp16", torch.float16, 8, 1, 128, 32, (65, 300), (64, 13), 10.0, 0, 1),
     ("int8", torch.bfloat16, 3, 2, 128, 4096, (4200,), (2,), 0.0, 0, 0),
-    # more than 16 query rows a key head: tiles of 128 on the tensor cores
+    # 17 to 32 query rows a key head, and more: tiles of 128 on the tensor cores
     ("int8", torch.float16, 1, 2, 64, 8, (700, 18, 40), (18, 17, 0), 0.0, 0, 1),
     ("bf16", torch.bfloat16, 32, 1, 64, 64, (1, 130, 129, 0), None, 15.0, 0, 0),
+    ("bf16", torch.bfloat16, 33, 1, 64, 64, (1, 130, 129, 0), None, 15.0, 0, 0),
+    ("int8", torch.bfloat16, 48, 1, 128, 16, (700, 129), None, 0.0, 1, 0),
     ("e4m3", torch.float16, 8, 1, 128, 16, (500, 60), (40, 33), 0.0, 1, 0),
     ("fp16", torch.float16, 20, 2, 128, 32, (1000, 3), None, 0.0, 0, 0),
     ("e4m3", torch.bfloat16, 5, 1, 64, 128, (3000, 64, 2), (64, 64, 2), 0.0, 0, 1),
@@ -219,8 +221,8 @@ def test_cache_attention(case):
 
 def test_cache_attention_long_and_many():
     """One long sequence over all SMs, and many short ones beside it: parts that end inside others."""
-    for lens, G in (((20000,), 4), (tuple([3] * 200 + [9000] + [130] * 60), 4), ((20000, 1), 24),
-                    (tuple([3] * 200 + [9000] + [130] * 60), 24)):
+    for lens, G in (((20000,), 4), (tuple([3] * 200 + [9000] + [130] * 60), 4), ((20000, 1), 24), ((20000, 1), 40),
+                    (tuple([3] * 200 + [9000] + [130] * 60), 40)):
         cache, table, ks, vs = filled("int8", lens, 2, 64, 64)
         q = randn((len(lens), 2 * G, 64), torch.bfloat16, 5, 1.5)
         ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -232,7 +234,7 @@ def test_cache_attention_long_and_many():
 def test_cache_attention_values_of_any_size():
     """Value rows of very different size in one 8-bit cache, and tiny ones: none underflows on the way."""
     lens = (70,)
-    for size, G in ((1e-18, 4), (1e12, 4), (1e-18, 17), (1e12, 17)):
+    for size, G in ((1e-18, 4), (1e12, 4), (1e-18, 17), (1e12, 17), (1e-18, 40), (1e12, 40)):
         cache, table, ks, vs = filled("e4m3", lens, 1, 64, 16, v_scale=size)
         q = randn((1, G, 64), torch.bfloat16, 5)
         ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -240,7 +242,7 @@ def test_cache_attention_values_of_any_size():
         du.check("o", lh.cache_attention(cache, q, table, ln), (value, bound))
 
 
-@pytest.mark.parametrize("G", [2, 20])
+@pytest.mark.parametrize("G", [2, 20, 40])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_bad_lengths_and_pages_are_cut_and_reported(kind, G):
     lens = (40, 20)
