@@ -9,6 +9,6 @@ from .api import (Buffers, Layer, LighthouseAttentionFn, attn_bwd, attn_bwd_rows
                   backward, check_error, forward, gather, lighthouse_attention, plan, pool_adjoint, pyramid_pool,
                   scatter_back, scatter_back_adjoint, score_topk)
 from .cache import KVCache, cache_attention, cache_read, cache_write  # noqa: F401
-from .dense import (AttentionMask, Rotary, apply_rotary, attention_mask, check_dense_error,  # noqa: F401
+from .dense import (AttentionMask, AttentionSaved, Rotary, apply_rotary, attention_mask, check_dense_error,  # noqa: F401
                     dense_attention, dense_backward, dense_forward, rotary, rotary_frequencies)
 from . import pisa  # noqa: F401

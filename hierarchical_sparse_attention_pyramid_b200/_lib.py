@@ -118,8 +118,8 @@ SIGNATURES = {
     "lh_rotary": [_RCFG, _P, _P, _P, _P, _P, _P, _P],
     "lh_mask_spans_bytes": [c_int64, c_int64],
     "lh_mask_spans": [c_int64, c_int64, c_int32, _P, _P, _P, _P],
-    "lh_dense_fwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P],
-    "lh_dense_bwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "lh_dense_fwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "lh_dense_bwd": [_DCFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "lh_cache_write": [_CACHE, c_int64, c_int32, _P, _P, _P, _P, _P, _P, _P],
     "lh_cache_read": [_CACHE, c_int32, c_int32, _P, _P, c_int64, c_int32, _P, _P, _P, _P],
     "lh_cache_attn_ws_bytes": [_CACHE, _ACFG],

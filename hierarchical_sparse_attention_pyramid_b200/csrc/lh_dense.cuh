@@ -206,10 +206,10 @@ bool make_head_map(CUtensorMap* m, const void* base, int dtype, int64_t B, int64
 cudaError_t launch_mask_spans(const int32_t* docs, const uint8_t* prefix, int64_t B, int N, int causal,
                               const SpanBuffer& s, cudaStream_t st);
 cudaError_t launch_dense_fwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
-                             const CUtensorMap& v, void* o, const Strides& so, cudaStream_t st);
+                             const CUtensorMap& v, void* o, const Strides& so, void* o_low, cudaStream_t st);
 cudaError_t launch_dense_bwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, const CUtensorMap& go, const void* o, const Strides& so,
-                             const void* dout, const Strides& sdo, void* dq, const Strides& sdq, void* dk,
+                             const void* o_low, const void* dout, const Strides& sdo, void* dq, const Strides& sdq, void* dk,
                              const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st);
 
 }  // namespace lh

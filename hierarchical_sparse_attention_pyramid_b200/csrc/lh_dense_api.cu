@@ -148,12 +148,13 @@ lh_status lh_mask_spans(int64_t B, int64_t N, int32_t causal, const int32_t* doc
 }
 
 lh_status lh_dense_fwd(const lh_dense_config* cfg, const void* q, const void* k, const void* v, const void* spans,
-                       const float* slopes, void* o, float* lse, void* err, lh_stream_t stream) {
+                       const float* slopes, void* o, void* o_low, float* lse, void* err, lh_stream_t stream) {
   const char* kCall = "lh_dense_fwd";
   const lh_status s = check_dense(cfg, kCall);
   if (s != LH_OK) return s;
   CHECK_PTR(q); CHECK_PTR(k); CHECK_PTR(v); CHECK_PTR(o); CHECK_PTR(lse);
   if (spans) CHECK_PTR(spans);
+  if (o_low) CHECK_PTR(o_low);
   if (((uintptr_t)slopes | (uintptr_t)err) & 3) return fail(LH_ERR_INVALID_ARG, kCall, "slopes or err: misaligned");
   CHECK_STRIDE(q_stride, cfg->Hq); CHECK_STRIDE(k_stride, cfg->Hkv); CHECK_STRIDE(v_stride, cfg->Hkv);
   CHECK_STRIDE(o_stride, cfg->Hq);
@@ -164,13 +165,13 @@ lh_status lh_dense_fwd(const lh_dense_config* cfg, const void* q, const void* k,
       !make_head_map(&mk, k, cfg->dtype, cfg->B, cfg->Hkv, cfg->N, cfg->d, cfg->k_stride) ||
       !make_head_map(&mv, v, cfg->dtype, cfg->B, cfg->Hkv, cfg->N, cfg->d, cfg->v_stride))
     return fail(LH_ERR_CUDA, kCall, "no tensor map for these strides");
-  return done(launch_dense_fwd(a, cfg->d, cfg->dtype == LH_FP16, mq, mk, mv, o, strides_of(cfg->o_stride),
+  return done(launch_dense_fwd(a, cfg->d, cfg->dtype == LH_FP16, mq, mk, mv, o, strides_of(cfg->o_stride), o_low,
                                (cudaStream_t)stream),
               kCall);
 }
 
 lh_status lh_dense_bwd(const lh_dense_config* cfg, const void* q, const void* k, const void* v, const void* o,
-                       const void* dout, const float* lse, const void* spans, const float* slopes, float* delta,
+                       const void* o_low, const void* dout, const float* lse, const void* spans, const float* slopes, float* delta,
                        void* dq, void* dk, void* dv, void* err, lh_stream_t stream) {
   const char* kCall = "lh_dense_bwd";
   const lh_status s = check_dense(cfg, kCall);
@@ -178,6 +179,7 @@ lh_status lh_dense_bwd(const lh_dense_config* cfg, const void* q, const void* k,
   CHECK_PTR(q); CHECK_PTR(k); CHECK_PTR(v); CHECK_PTR(o); CHECK_PTR(dout); CHECK_PTR(lse); CHECK_PTR(delta);
   CHECK_PTR(dq); CHECK_PTR(dk); CHECK_PTR(dv);
   if (spans) CHECK_PTR(spans);
+  if (o_low) CHECK_PTR(o_low);
   if (((uintptr_t)slopes | (uintptr_t)err) & 3) return fail(LH_ERR_INVALID_ARG, kCall, "slopes or err: misaligned");
   CHECK_STRIDE(q_stride, cfg->Hq); CHECK_STRIDE(k_stride, cfg->Hkv); CHECK_STRIDE(v_stride, cfg->Hkv);
   CHECK_STRIDE(o_stride, cfg->Hq); CHECK_STRIDE(do_stride, cfg->Hq); CHECK_STRIDE(dq_stride, cfg->Hq);
@@ -191,7 +193,7 @@ lh_status lh_dense_bwd(const lh_dense_config* cfg, const void* q, const void* k,
       !make_head_map(&mv, v, cfg->dtype, cfg->B, cfg->Hkv, cfg->N, cfg->d, cfg->v_stride) ||
       !make_head_map(&mo, dout, cfg->dtype, cfg->B, cfg->Hq, cfg->N, cfg->d, cfg->do_stride))
     return fail(LH_ERR_CUDA, kCall, "no tensor map for these strides");
-  return done(launch_dense_bwd(a, cfg->d, cfg->dtype == LH_FP16, mq, mk, mv, mo, o, strides_of(cfg->o_stride), dout,
+  return done(launch_dense_bwd(a, cfg->d, cfg->dtype == LH_FP16, mq, mk, mv, mo, o, strides_of(cfg->o_stride), o_low, dout,
                                strides_of(cfg->do_stride), dq, strides_of(cfg->dq_stride), dk,
                                strides_of(cfg->dk_stride), dv, strides_of(cfg->dv_stride), (cudaStream_t)stream),
               kCall);

@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dense_bwd_q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                        const __grid_constant__ DenseArgs a, const void* __restrict__ O, const Strides so,
-                       const void* __restrict__ dO, const Strides sdo, void* __restrict__ dQ, const Strides sdq) {
+                       const void* __restrict__ Olow, const void* __restrict__ dO, const Strides sdo, void* __restrict__ dQ, const Strides sdq) {
   using Lay = QSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -632,31 +632,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = (warp & 3) * 32 + lane;  // query row of the tile (TMEM lane)
     const int q = qt * 128 + t;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    // Delta of the row: each warpgroup sums half of the channels
+    // Delta of the tile's rows, a warp 16 of them
     float* sDel = reinterpret_cast<float*>(smem + Lay::oDel);
-    {
-      float sum = 0.f;
-      if (NJ != 1 && q < a.N) {
-        const uint4* o4 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(O) + b * so.b + h * so.h +
-                                                         (int64_t)q * so.n + g * (D / 2));
-        const uint4* g4 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(dO) + b * sdo.b +
-                                                         h * sdo.h + (int64_t)q * sdo.n + g * (D / 2));
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 u = __ldg(o4 + i), w = __ldg(g4 + i);
-          const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, wa[4] = {w.x, w.y, w.z, w.w};
+    if (NJ != 1) {
+      constexpr int L = D / 8, R = 32 / L;  // lanes of a row, rows of a warp at a time
+#pragma unroll 4
+      for (int i = 0; i < 16 / R; ++i) {
+        const int r = warp * 16 + i * R + lane / L, qq = qt * 128 + r, c = lane % L * 8;
+        float sum = 0.f;
+        if (qq < a.N) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(O) + b * so.b +
+                                                               h * so.h + (int64_t)qq * so.n + c));
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(dO) + b * sdo.b +
+                                                               h * sdo.h + (int64_t)qq * sdo.n + c));
+          const uint4 v = Olow ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(Olow) +
+                                                                      ((int64_t)bh * a.N + qq) * D + c))
+                               : make_uint4(0, 0, 0, 0);
+          const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, wa[4] = {w.x, w.y, w.z, w.w}, va[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 x = unpack2<F16>(ua[e]), y = unpack2<F16>(wa[e]);
-            sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+            const float2 x = unpack2<F16>(ua[e]), y = unpack2<F16>(wa[e]), z = unpack2<F16>(va[e]);
+            sum = fmaf(x.x + z.x, y.x, fmaf(x.y + z.y, y.y, sum));
           }
         }
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane % L == 0) sDel[r] = sum;
       }
-      sDel[g * 128 + t] = sum;
     }
     compute_sync_q();
-    float del = sDel[t] + sDel[128 + t];
-        const float lse_raw = q < a.N ? a.lse[(int64_t)bh * a.N + q] : -INFINITY;
+    float del = NJ != 1 ? sDel[t] : 0.f;
+    const float lse_raw = q < a.N ? a.lse[(int64_t)bh * a.N + q] : -INFINITY;
     const float lse = lse_raw == -INFINITY ? INFINITY : lse_raw * kLog2e;  // no key: P = 2^-inf = 0
     const float scale_log2 = a.scale * kLog2e;
     const uint64_t c2 = f2_pack(scale_log2, scale_log2);
@@ -726,10 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, mbar_wait(bDP, j & 1, abort_flag));
       if (NJ == 1) {
-        // The row's keys all lie in this tile: Delta = sum_j P dP in fp32
-        // instead of from the rounded O.  With two or three keys, one of them
-        // nearly all of the weight, dP - Delta is a small difference that the
-        // rounding of O would swamp; over more keys it averages out.
+        // The row's keys all lie in this tile: Delta = sum_j P dP in fp32.
+        // With two or three keys, one of them nearly all of the weight,
+        // dP - Delta is a small difference, which the roundings of P in O,
+        // averaged over more keys, would still show in.
         float sum = 0.f;
         if (ok) {
           tc_fence_after();
@@ -840,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, bool F16, bool MOD>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& go,
-                   const DenseArgs& a, const void* o, const Strides& so, const void* dout, const Strides& sdo, void* dq,
+                   const DenseArgs& a, const void* o, const Strides& so, const void* o_low, const void* dout, const Strides& sdo, void* dq,
                    const Strides& sdq, void* dk, const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st) {
   const int64_t gq = (int64_t)a.n_tiles * a.B * a.Hq, gk = (int64_t)a.n_tiles * a.B * a.Hkv;
   if (gq > 0x7fffffffll) return cudaErrorInvalidConfiguration;
@@ -850,7 +856,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(fk, cudaFuncAttributeMaxDynamicSharedMemorySize, KvSmem<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  fq<<<dim3((unsigned)gq), kThreads, QSmem<D>::kAlloc, st>>>(q, k, v, go, a, o, so, dout, sdo, dq, sdq);
+  fq<<<dim3((unsigned)gq), kThreads, QSmem<D>::kAlloc, st>>>(q, k, v, go, a, o, so, o_low, dout, sdo, dq, sdq);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Few key tiles leave SMs idle: then a cluster of 2, 4 or 8 CTAs shares the
@@ -878,11 +884,11 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
 
 cudaError_t launch_dense_bwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, const CUtensorMap& go, const void* o, const Strides& so,
-                             const void* dout, const Strides& sdo, void* dq, const Strides& sdq, void* dk,
+                             const void* o_low, const void* dout, const Strides& sdo, void* dq, const Strides& sdq, void* dk,
                              const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st) {
   const bool mod = a.softcap > 0.f || a.slopes;
   auto pick = [&](auto D, auto F, auto M) {
-    return launch<decltype(D)::value, decltype(F)::value, decltype(M)::value>(q, k, v, go, a, o, so, dout, sdo, dq,
+    return launch<decltype(D)::value, decltype(F)::value, decltype(M)::value>(q, k, v, go, a, o, so, o_low, dout, sdo, dq,
                                                                               sdq, dk, sdk, dv, sdv, st);
   };
   using T = std::true_type;

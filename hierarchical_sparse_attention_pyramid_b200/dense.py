@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -282,6 +283,12 @@ def attention_mask(docs=None, prefix=None, causal: bool = True) -> AttentionMask
 
 # ------------------------------------------------------------------ attention
 
+class AttentionSaved(NamedTuple):
+    """What dense_forward leaves for dense_backward beside the output."""
+    lse: torch.Tensor           # [B, Hq, N] fp32, log of the row's sum of exponentials
+    o_low: torch.Tensor | None  # [B, Hq, N, d] in the inputs' type: what rounding the output took off
+
+
 def _dense_config(q, k, v, mask, causal, scale, softcap, slopes):
     _tensor("q", q)
     if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16):
@@ -306,12 +313,13 @@ def _dense_config(q, k, v, mask, causal, scale, softcap, slopes):
 
 
 def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = True, scale: float | None = None,
-                  softcap: float = 0.0, slopes=None):
-    """Masked attention of q [B, Hq, N, d] over k, v [B, Hkv, N, d], bf16 or fp16 -> (o as q, lse [B, Hq, N] fp32).
+                  softcap: float = 0.0, slopes=None, for_backward: bool = True):
+    """Masked attention of q [B, Hq, N, d] over k, v [B, Hkv, N, d], bf16 or fp16 -> (o as q, AttentionSaved).
 
     mask: from attention_mask (causal is then the mask's); None: causal or full.  scale: 1/sqrt(d) unless given.
     softcap > 0: scores x become softcap * tanh(x / softcap).  slopes: fp32 [Hq], scores get -slope |i - j|.
-    A query without keys gets o = 0, lse = -inf."""
+    A query without keys gets o = 0, lse = -inf.  for_backward False leaves o_low out: dense_backward then takes its
+    row sums from the rounded output, which costs accuracy where few keys carry a row."""
     for name, t in (("q", q), ("k", k), ("v", v)):
         _is_tensor(name, t)
     key = ("dense_forward", _sig(q), _sig(k), _sig(v), None if mask is None else (mask.B, mask.N, _sig(mask.spans)),
@@ -325,18 +333,21 @@ def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = Tru
     cfg, rows, o_stride = plan
     o = torch.empty_strided(q.shape, o_stride, dtype=q.dtype, device=q.device)
     lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+    low = torch.empty(q.shape, dtype=q.dtype, device=q.device) if for_backward else None
     index = q.device.index
     _call("lh_dense_fwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          None if mask is None else mask.spans.data_ptr(), _ptr(slopes), o.data_ptr(), lse.data_ptr(), _err(index))
-    return o, lse
+          None if mask is None else mask.spans.data_ptr(), _ptr(slopes), o.data_ptr(), _ptr(low), lse.data_ptr(),
+          _err(index))
+    return o, AttentionSaved(lse, low)
 
 
-def dense_backward(do, q, k, v, o, lse, mask: AttentionMask | None = None, causal: bool = True,
+def dense_backward(do, q, k, v, o, saved: AttentionSaved, mask: AttentionMask | None = None, causal: bool = True,
                    scale: float | None = None, softcap: float = 0.0, slopes=None):
-    """Gradients of dense_forward's o with its inputs, o and lse -> (dq, dk, dv)."""
+    """Gradients of dense_forward's o with its inputs and both of its results -> (dq, dk, dv)."""
+    lse, low = saved
     for name, t in (("do", do), ("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse)):
         _is_tensor(name, t)
-    key = ("dense_backward", _sig(do), _sig(q), _sig(k), _sig(v), _sig(o), _sig(lse),
+    key = ("dense_backward", _sig(do), _sig(q), _sig(k), _sig(v), _sig(o), _sig(lse), _sig(low),
            None if mask is None else (mask.B, mask.N, _sig(mask.spans)), causal, scale, softcap, _sig(slopes))
     plan = _plans.get(key)
     if plan is None:
@@ -346,6 +357,8 @@ def dense_backward(do, q, k, v, o, lse, mask: AttentionMask | None = None, causa
             if not _addressable(t):
                 raise ValueError(f"{name}: strides {t.stride()}, expected contiguous channels in 16-byte rows")
         _flat("lse", lse, q.device, torch.float32, q.shape[:3])
+        if low is not None:
+            _flat("o_low", low, q.device, q.dtype, q.shape)
         grads = [_like(t) for t in (q, k, v)]
         cfg.o_stride, cfg.do_stride = _strides(o), _strides(do)
         cfg.dq_stride, cfg.dk_stride, cfg.dv_stride = (_strides(g) for g in grads)
@@ -355,8 +368,8 @@ def dense_backward(do, q, k, v, o, lse, mask: AttentionMask | None = None, causa
                   for t, s in zip((q, k, v), strides))
     delta = torch.empty_like(lse)
     index = q.device.index
-    _call("lh_dense_bwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-          lse.data_ptr(), None if mask is None else mask.spans.data_ptr(), _ptr(slopes), delta.data_ptr(),
+    _call("lh_dense_bwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(low),
+          do.data_ptr(), lse.data_ptr(), None if mask is None else mask.spans.data_ptr(), _ptr(slopes), delta.data_ptr(),
           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _err(index))
     return dq, dk, dv
 
@@ -377,15 +390,16 @@ class _DenseAttentionFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, slopes, mask, opt):
         q, k, v = _usable(q), _usable(k), _usable(v)
-        o, lse = dense_forward(q, k, v, mask, slopes=slopes, **opt)
-        ctx.save_for_backward(q, k, v, o, lse)
+        o, saved = dense_forward(q, k, v, mask, slopes=slopes, for_backward=any(ctx.needs_input_grad[:3]), **opt)
+        ctx.save_for_backward(q, k, v, o, *saved)
         ctx.slopes, ctx.mask, ctx.opt = slopes, mask, opt
         return o
 
     @staticmethod
     def backward(ctx, do):
-        q, k, v, o, lse = ctx.saved_tensors
-        dq, dk, dv = dense_backward(_usable(do), q, k, v, o, lse, ctx.mask, slopes=ctx.slopes, **ctx.opt)
+        q, k, v, o, lse, low = ctx.saved_tensors
+        dq, dk, dv = dense_backward(_usable(do), q, k, v, o, AttentionSaved(lse, low), ctx.mask, slopes=ctx.slopes,
+                                    **ctx.opt)
         return dq, dk, dv, None, None, None
 
 

@@ -501,22 +501,24 @@ typedef struct {
  * fp32 (>= 0 for a penalty) or NULL.  Strides are multiples of 8 elements and
  * pointers 16-byte aligned.
  * Out: o; lse [B][Hq][N] fp32, the natural log of the row's sum of
- * exponentials.  A query without keys has O = 0 and LSE = -inf.
+ * exponentials; o_low [B][Hq][N][d] in the inputs' type, contiguous, or NULL:
+ * what rounding to o took off (for lh_dense_bwd).  A query without keys has O = 0 and LSE = -inf.
  * Probabilities enter P V rounded to the inputs' type; sums are fp32.  Values
  * in padding and past N are not used; those of another document of the batch
  * row must be finite. */
 lh_status lh_dense_fwd(const lh_dense_config *cfg, const void *q, const void *k, const void *v, const void *spans,
-                       const float *slopes, void *o, float *lse, void *err, lh_stream_t stream);
+                       const float *slopes, void *o, void *o_low, float *lse, void *err, lh_stream_t stream);
 
 /* Its gradients (none for the slopes), dK and dV summed over the query heads
  * that share a key head; every gradient is written once, in an order that does
  * not depend on scheduling.  Probabilities are recomputed from the fp32 LSE,
  * whose rounding is theirs: 2^-24 |LSE| relative, which scores of up to 2^12 in
- * size keep below the gradients' own rounding.  In: the forward's inputs, o and lse, and dout.
+ * size keep below the gradients' own rounding.  In: the forward's inputs, o,
+ * o_low (NULL: delta from the rounded o) and lse, and dout.
  * Scratch: delta [B][Hq][N] fp32 (left holding rowsum(dout * o)). */
 lh_status lh_dense_bwd(const lh_dense_config *cfg, const void *q, const void *k, const void *v, const void *o,
-                       const void *dout, const float *lse, const void *spans, const float *slopes, float *delta,
-                       void *dq, void *dk, void *dv, void *err, lh_stream_t stream);
+                       const void *o_low, const void *dout, const float *lse, const void *spans, const float *slopes,
+                       float *delta, void *dq, void *dk, void *dv, void *err, lh_stream_t stream);
 
 /* A paged key/value cache, as the dense attention is served.  k and v are
  * [pages][heads][page][d] in the held type; the 8-bit kinds keep one fp32 scale

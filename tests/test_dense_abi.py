@@ -68,20 +68,22 @@ DENSE_BAD = [
 @pytest.mark.parametrize("kw,status", DENSE_BAD)
 def test_dense_refusals(lib, kw, status):
     c = ctypes.byref(dense_config(**kw))
-    assert lib.lh_dense_fwd(c, FAKE, FAKE, FAKE, None, None, FAKE, FAKE, None, None) == status
-    assert lib.lh_dense_bwd(c, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, None, None) == status
+    assert lib.lh_dense_fwd(c, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, None, None) == status
+    assert lib.lh_dense_bwd(c, *[FAKE] * 4, None, FAKE, FAKE, None, None, *[FAKE] * 4, None, None) == status
     assert lib.lh_last_error_message()
 
 
 def test_dense_pointers(lib):
     c = ctypes.byref(dense_config())
-    args = [FAKE, FAKE, FAKE, None, None, FAKE, FAKE, None]
-    for i in (0, 1, 2, 5, 6):
+    args = [FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, None]
+    for i in (0, 1, 2, 5, 7):
         for bad in (None, ODD):
             assert lib.lh_dense_fwd(c, *args[:i], bad, *args[i + 1:], None) == 1
     assert lib.lh_dense_fwd(c, *args[:3], ODD, *args[4:], None) == 1  # spans
-    back = [FAKE] * 6 + [None, None] + [FAKE] * 4 + [None]
-    for i in (0, 1, 2, 3, 4, 5, 8, 9, 10, 11):
+    assert lib.lh_dense_fwd(c, *args[:6], ODD, *args[7:], None) == 1  # o_low
+    back = [FAKE] * 4 + [None] + [FAKE] * 2 + [None, None] + [FAKE] * 4 + [None]
+    assert lib.lh_dense_bwd(c, *back[:4], ODD, *back[5:], None) == 1
+    for i in (0, 1, 2, 3, 5, 6, 9, 10, 11, 12):
         for bad in (None, ODD):
             assert lib.lh_dense_bwd(c, *back[:i], bad, *back[i + 1:], None) == 1
     for n in ("do", "dq", "dk", "dv"):

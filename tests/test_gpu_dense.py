@@ -183,10 +183,10 @@ def run_dense(case, tensors):
     causal, cap = case[8], case[9]
     mask = lh.attention_mask(ids, pre, causal=causal) if ids is not None or pre is not None else None
     opt = dict(mask=mask, causal=causal, softcap=cap, slopes=slopes)
-    o, lse = lh.dense_forward(q, k, v, **opt)
-    grads = lh.dense_backward(do, q, k, v, o, lse, **opt)
+    o, saved = lh.dense_forward(q, k, v, **opt)
+    grads = lh.dense_backward(do, q, k, v, o, saved, **opt)
     lh.check_dense_error()
-    return dict(zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)))
+    return dict(zip(("o", "lse", "dq", "dk", "dv"), (o, saved.lse, *grads)))
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
@@ -234,7 +234,7 @@ def test_scores_of_the_lowest_values():
     q, k, v = (torch.ones(1, 1, 130, 64, dtype=torch.bfloat16, device="cuda") for _ in range(3))
     k[0, 0, :64] = -3e28
     v[0, 0] = torch.arange(130, device="cuda")[:, None].bfloat16()
-    o, lse = lh.dense_forward(q, k, v)
+    o, (lse, _) = lh.dense_forward(q, k, v)
     i = torch.arange(130, device="cuda").double()
     # rows below 64 see equal scores of -2.4e29 each (exact in fp32: a sum of 64 equal terms), later rows the others
     want = torch.where(i < 64, i / 2, (64 + i) / 2)
@@ -322,12 +322,12 @@ def test_streams_and_graphs():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         mask = lh.attention_mask(t[4], t[5])
-        o, lse = lh.dense_forward(*static[:3], mask=mask, softcap=10.0)
-        grads = lh.dense_backward(static[3], *static[:3], o, lse, mask=mask, softcap=10.0)
+        o, saved = lh.dense_forward(*static[:3], mask=mask, softcap=10.0)
+        grads = lh.dense_backward(static[3], *static[:3], o, saved, mask=mask, softcap=10.0)
     for src, want_ in ((t, want), (other, want2)):
         for a, b in zip(static, src[:4]):
             a.copy_(b)
         graph.replay()
         torch.cuda.synchronize()
-        for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, saved.lse, *grads)):
             assert torch.equal(x, want_[n]), n
