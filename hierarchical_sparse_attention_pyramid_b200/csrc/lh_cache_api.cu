@@ -25,7 +25,8 @@ lh_status check_cache(const lh_cache* c, const char* call, CacheView* v) {
   if (c->page < 8 || c->page > 4096 || (c->page & (c->page - 1)) != 0)
     return fail(LH_ERR_UNSUPPORTED, call, "page must be a power of two in [8, 4096]");
   if (c->kind < LH_CACHE_BF16 || c->kind > LH_CACHE_INT8) return fail(LH_ERR_INVALID_ARG, call, "bad kind");
-  if (c->pages > 0x7fffffffll || c->heads > 65535 || c->pages * c->heads > 0xfffffffell / c->page) return fail(LH_ERR_UNSUPPORTED, call, "too many pages or heads");
+  if (c->pages > 0x7fffffffll || c->heads > 65535 || c->pages * c->heads > 0xfffffffell / c->page)
+    return fail(LH_ERR_UNSUPPORTED, call, "too many pages or heads");
   if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
     return fail(LH_ERR_INVALID_ARG, call, "k, v: NULL or not 16-byte aligned");
   const bool held8 = c->kind == LH_CACHE_E4M3 || c->kind == LH_CACHE_INT8;

@@ -533,53 +533,17 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
   }
 }
 
-// Joins the pieces of every query row that lie in several blocks.  W warps
-// take a row (8 where a row has many pieces, else one, and a block 8 rows):
-// they share its pieces out and are joined in warp order.
-constexpr int kJoinWarps = 8;
+// the block that has unit u (block c of `blocks` takes [total c / blocks, total (c + 1) / blocks))
+__device__ __forceinline__ int block_of(int64_t u, int64_t total, int blocks) {
+  return (int)(((u + 1) * blocks + total - 1) / total - 1);
+}
+
+// row r of a tile whose pieces the blocks [c0, c1] have, into row `out` of the output
 template <int D, bool F16, int W>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a, int rows_per_tile, int blocks) {
-  __shared__ float sO[W == 1 ? 1 : W][D];
-  __shared__ float sL[kJoinWarps], sM[kJoinWarps];
+__device__ __forceinline__ void join_row(const CacheAttnArgs& a, int rows_per_tile, int c0, int c1, int r, int64_t out,
+                                         float (*sO)[D], float* sL, float* sM) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t out = W == 1 ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x;
-  const int tok = (int)(out / a.Hq), head = (int)(out % a.Hq), G = a.Hq / a.c.heads;
-  int s = tok;
-  if (a.q_start) {
-    int lo = 0, hi = a.seqs;  // the last sequence whose first token is not after this one
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.q_start + mid) <= tok) lo = mid;
-      else hi = mid - 1;
-    }
-    s = lo;
-  }
-  const Seq seq = s < a.seqs ? load_seq(a, s, false) : Seq{0, 0, 0};
-  // units before the sequence, and of all (every warp adds them up)
-  int64_t before = 0, all = 0;
-  for (int i = lane; i < a.seqs; i += 32) {
-    const int64_t n = seq_units(a, load_seq(a, i, false), rows_per_tile);
-    all += n;
-    if (i < s) before += n;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, d);
-    before += __shfl_xor_sync(0xffffffffu, before, d);
-  }
-  const int r = (tok - seq.tok0) * G + head % G, kt_n = key_units(seq.len);
-  const int row_tiles = (seq.T * G + rows_per_tile - 1) / rows_per_tile;
-  const int64_t end = before + (int64_t)(head / G * row_tiles + r / rows_per_tile + 1) * kt_n;
-  // block c of nb takes the units [all c / nb, all (c + 1) / nb)
-  const int64_t nb = min((int64_t)blocks, all);
-  auto block_of = [&](int64_t u) { return (int)(((u + 1) * nb + all - 1) / all - 1); };
-  // a token of no sequence is left as it is
-  const bool live = out < a.n_tok * a.Hq && tok >= seq.tok0 && tok < seq.tok0 + seq.T;
-  const int c0 = live ? block_of(end - kt_n + kBegin) : 0, c1 = live ? block_of(end - 1) : 0;
-  cudaGridDependencySynchronize();  // every block: what follows in the stream waits for this kernel alone
-  if (c0 == c1) return;  // written by that block (W > 1: the whole block's row)
-  auto place = [&](int c) { return ((int64_t)c * 2 + (c == c0)) * rows_per_tile + r % rows_per_tile; };
+  auto place = [&](int c) { return ((int64_t)c * 2 + (c == c0)) * rows_per_tile + r; };
   float mm = -INFINITY;
   for (int c = c0 + (W == 1 ? lane : (int)threadIdx.x); c <= c1; c += W * 32) mm = fmaxf(mm, a.part_ml[place(c)].x);
 #pragma unroll
@@ -624,6 +588,74 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   for (int i = 0; i < C; i += 2) dst[i / 2] = pack2<F16>(o[i] * inv, o[i + 1] * inv);
 }
 
+// Joins the pieces of the query rows that lie in several blocks.
+//
+// Rows in few pieces (W = 1): blocks (x, ..) take the rows of the one
+// (sequence, head, row tile) that block x of the work began and did not finish,
+// if there is one, a warp a row at a time.  The work then goes by the blocks and
+// not by the rows of the call, most of which one block has whole: 4096
+// sequences, 32 query heads: 19 us, and 1.3 ms with a warp for every row.
+// Rows in many pieces, of which there are few (W = 8): block (i, r) takes row r
+// of the i-th (sequence, head, row tile); its warps share the pieces out and are
+// joined in warp order.  One sequence of 512K tokens: 7 us, 18 us by blocks.
+constexpr int kJoinWarps = 8;
+template <int D, bool F16, int W>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a, int rows_per_tile) {
+  __shared__ float sO[W == 1 ? 1 : W][D];
+  __shared__ float sL[kJoinWarps], sM[kJoinWarps];
+  __shared__ int64_t scan[kJoinWarps + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.Hq / a.c.heads;
+  Seq seq{0, 0, 0};
+  int hk = 0, rt = 0, c0 = 0, c1 = 0;
+  if constexpr (W == 1) {
+    const Stretch st = find_stretch<kJoinWarps, true>(a, rows_per_tile, scan);
+    if (st.u < st.u_end) {
+      seq = load_seq(a, st.s, false);
+      const int kt_n = key_units(seq.len), tiles = (seq.T * G + rows_per_tile - 1) / rows_per_tile;
+      const int inst = (int)(st.in_seq / kt_n), last = (int)(st.in_seq % kt_n);
+      const int64_t first = st.u_end - 1 - last;  // its first unit
+      hk = inst / tiles, rt = inst % tiles;
+      c0 = c1 = blockIdx.x;
+      if (last >= kBegin && first + kBegin >= st.u && last + 1 < kt_n)  // some keys here, the first ones, and not all
+        c1 = block_of(first + kt_n - 1, st.total, st.blocks);
+    }
+  } else {
+    const int tiles_most = ((int)(a.max_tokens * (int64_t)G) + rows_per_tile - 1) / rows_per_tile;
+    const int s = blockIdx.x / (a.c.heads * tiles_most);
+    hk = blockIdx.x / tiles_most % a.c.heads;
+    rt = blockIdx.x % tiles_most;
+    int64_t before = 0, total = 0;  // units before the sequence, and of all
+    for (int i = lane; i < a.seqs; i += 32) {
+      const int64_t n = seq_units(a, load_seq(a, i, false), rows_per_tile);
+      total += n;
+      if (i < s) before += n;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, d);
+      before += __shfl_xor_sync(0xffffffffu, before, d);
+    }
+    seq = load_seq(a, s, false);
+    const int kt_n = key_units(seq.len), tiles = (seq.T * G + rows_per_tile - 1) / rows_per_tile;
+    if (rt < tiles) {
+      const int64_t end = before + (int64_t)(hk * tiles + rt + 1) * kt_n;
+      const int blocks = (int)min((int64_t)a.blocks, total);
+      c0 = block_of(end - kt_n + kBegin, total, blocks);
+      c1 = block_of(end - 1, total, blocks);
+    }
+  }
+  cudaGridDependencySynchronize();  // every block: what follows in the stream waits for this kernel alone
+  if (c0 == c1) return;             // written by that block
+#pragma unroll 1
+  for (int r = W == 1 ? blockIdx.y * kJoinWarps + warp : blockIdx.y; r < rows_per_tile; r += gridDim.y * (kJoinWarps / W)) {
+    const int row = rt * rows_per_tile + r;
+    if (row >= seq.T * G) break;
+    join_row<D, F16, W>(a, rows_per_tile, c0, c1, r, (int64_t)(seq.tok0 + row / G) * a.Hq + hk * G + row % G, sO, sL,
+                        sM);
+  }
+}
+
 template <int D, int KIND, bool F16, int NB>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   constexpr int smem = Shape<D, KIND, NB>::kSmem;
@@ -653,13 +685,14 @@ cudaError_t by_kind(const CacheAttnArgs& a, int tile, cudaStream_t st) {
 
 template <int D, bool F16>
 cudaError_t join(const CacheAttnArgs& a, int rows_per_tile, cudaStream_t st) {
-  const int64_t rows = a.n_tok * a.Hq;
   const int64_t tiles = (int64_t)a.seqs * a.c.heads *
                         (((int64_t)a.max_tokens * (a.Hq / a.c.heads) + rows_per_tile - 1) / rows_per_tile);
   const bool many = a.blocks >= 8 * tiles;  // pieces of a row
   // it may be brought up while the pieces run; it waits for them itself
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(many ? rows : (rows + kJoinWarps - 1) / kJoinWarps));
+  // W = 1: up to 4 rows a warp, so that finding the place in the work list is shared
+  cfg.gridDim = many ? dim3((unsigned)tiles, (unsigned)rows_per_tile)
+                     : dim3((unsigned)a.blocks, (unsigned)(rows_per_tile <= 4 * kJoinWarps ? rows_per_tile / kJoinWarps : 4));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -667,8 +700,8 @@ cudaError_t join(const CacheAttnArgs& a, int rows_per_tile, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 8>, a, rows_per_tile, a.blocks)
-              : cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 1>, a, rows_per_tile, a.blocks);
+  return many ? cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 8>, a, rows_per_tile)
+              : cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 1>, a, rows_per_tile);
 }
 
 }  // namespace

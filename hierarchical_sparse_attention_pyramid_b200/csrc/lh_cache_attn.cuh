@@ -49,13 +49,14 @@ __device__ __forceinline__ int64_t seq_units(const CacheAttnArgs& a, const Seq& 
 // A block's place in the work list, by all of its threads (WARPS warps).
 struct Stretch {
   int64_t u, u_end;  // its units [u, u_end)
-  int64_t in_seq;    // u within its sequence
+  int64_t in_seq;    // u (or the last of them) within its sequence
+  int64_t total;     // units of the call
   int s;             // sequence
   int blocks;        // blocks that have any
 };
 // scan: WARPS + 1 int64 of shared memory.  A thread sums the units of a run of
-// sequences; the one whose run holds the first unit looks for its sequence.
-template <int WARPS>
+// sequences; the one whose run holds the first unit (LAST: the last one) looks for its sequence.
+template <int WARPS, bool LAST = false>
 __device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int rows_per_tile, int64_t* scan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (a.seqs + WARPS * 32 - 1) / (WARPS * 32);
@@ -79,15 +80,17 @@ __device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int rows
   before += incl - mine;
   Stretch r;
   r.blocks = (int)min((int64_t)gridDim.x, total);  // no block of these has an empty stretch
+  r.total = total;
   r.u = r.u_end = r.in_seq = 0;
   r.s = 0;
   if (blockIdx.x >= r.blocks) return r;
   r.u = total * blockIdx.x / r.blocks;
   r.u_end = total * (blockIdx.x + 1) / r.blocks;
+  const int64_t wanted = LAST ? r.u_end - 1 : r.u;
   __syncthreads();
-  if (r.u >= before && r.u < before + mine) {
+  if (wanted >= before && wanted < before + mine) {
     int i = s0;
-    int64_t at = r.u - before;
+    int64_t at = wanted - before;
     for (;;) {
       const int64_t n = seq_units(a, load_seq(a, i, false), rows_per_tile);
       if (at < n) break;

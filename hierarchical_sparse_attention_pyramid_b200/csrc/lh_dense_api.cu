@@ -171,8 +171,8 @@ lh_status lh_dense_fwd(const lh_dense_config* cfg, const void* q, const void* k,
 }
 
 lh_status lh_dense_bwd(const lh_dense_config* cfg, const void* q, const void* k, const void* v, const void* o,
-                       const void* o_low, const void* dout, const float* lse, const void* spans, const float* slopes, float* delta,
-                       void* dq, void* dk, void* dv, void* err, lh_stream_t stream) {
+                       const void* o_low, const void* dout, const float* lse, const void* spans, const float* slopes,
+                       float* delta, void* dq, void* dk, void* dv, void* err, lh_stream_t stream) {
   const char* kCall = "lh_dense_bwd";
   const lh_status s = check_dense(cfg, kCall);
   if (s != LH_OK) return s;
@@ -193,8 +193,8 @@ lh_status lh_dense_bwd(const lh_dense_config* cfg, const void* q, const void* k,
       !make_head_map(&mv, v, cfg->dtype, cfg->B, cfg->Hkv, cfg->N, cfg->d, cfg->v_stride) ||
       !make_head_map(&mo, dout, cfg->dtype, cfg->B, cfg->Hq, cfg->N, cfg->d, cfg->do_stride))
     return fail(LH_ERR_CUDA, kCall, "no tensor map for these strides");
-  return done(launch_dense_bwd(a, cfg->d, cfg->dtype == LH_FP16, mq, mk, mv, mo, o, strides_of(cfg->o_stride), o_low, dout,
-                               strides_of(cfg->do_stride), dq, strides_of(cfg->dq_stride), dk,
+  return done(launch_dense_bwd(a, cfg->d, cfg->dtype == LH_FP16, mq, mk, mv, mo, o, strides_of(cfg->o_stride), o_low,
+                               dout, strides_of(cfg->do_stride), dq, strides_of(cfg->dq_stride), dk,
                                strides_of(cfg->dk_stride), dv, strides_of(cfg->dv_stride), (cudaStream_t)stream),
               kCall);
 }
