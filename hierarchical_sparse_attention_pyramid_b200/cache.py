@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 
 import torch
 
@@ -19,7 +20,13 @@ _KINDS = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float8_e4m3fn: "e
 
 class KVCache:
     """The tensors of a paged cache: k, v [pages, heads, page, d] of bf16, fp16, float8_e4m3fn or int8 and, for the
-    8-bit types, k_scale, v_scale [pages, heads, page] fp32.  KVCache.empty allocates them."""
+    8-bit types, k_scale, v_scale [pages, heads, page] fp32.  KVCache.empty allocates them.  The tensors of a KVCache
+    stay the ones it was made of: the library holds their addresses."""
+
+    def __setattr__(self, name, value):
+        if "ref" in self.__dict__:
+            raise AttributeError(f"{name}: a KVCache is made anew for other tensors")
+        super().__setattr__(name, value)
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _is_tensor("k", k)
@@ -96,11 +103,14 @@ def cache_read(cache: KVCache, page_table, starts, total: int, dtype=torch.bfloa
     they are (uninitialised without out)."""
     for name, t in (("page_table", page_table), ("starts", starts)):
         _is_tensor(name, t)
+    total = operator.index(total)
     key = ("cache_read", cache.sig, _sig(page_table), _sig(starts), total, dtype)
     plan = _plans.get(key)
     if plan is None:
         seqs, width = _table(cache, page_table)
         _flat("starts", starts, cache.device, torch.int32, (seqs + 1,))
+        if total < 0:
+            raise ValueError(f"total: {total}, expected 0 or more")
         if dtype not in _NAMES:
             raise ValueError(f"dtype: {dtype}, expected bf16, fp16 or fp32")
         plan = _keep(key, (seqs, width, _lib.DENSE_DTYPES[_NAMES[dtype]], (total, cache.heads, cache.d)))
@@ -128,6 +138,7 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
     token u of its sequence where bit u is set.  scale, softcap, slopes: as dense_forward."""
     for name, t in (("q", q), ("page_table", page_table), ("lens", lens)):
         _is_tensor(name, t)
+    scale, softcap, max_tokens = None if scale is None else float(scale), float(softcap), operator.index(max_tokens)
     key = ("cache_attention", cache.sig, _sig(q), _sig(page_table), _sig(lens), _sig(q_start), max_tokens,
            _sig(tree_mask), scale, softcap, _sig(slopes))
     plan = _plans.get(key)

@@ -19,6 +19,7 @@ from dataclasses import dataclass
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import LhDenseConfig, LhRotaryConfig
@@ -177,10 +178,13 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
     for name, t in zip(("q", "k"), ts):
         _is_tensor(name, t)
     _is_tensor("frequencies", frequencies)
+    amplitude, inverse = float(amplitude), bool(inverse)
     if out is None:
         outs = [torch.empty_like(t) for t in ts]
     else:
         outs = list(out)[:len(ts)]
+        if len(outs) < len(ts):
+            raise ValueError(f"out: {len(outs)} tensors, expected {len(ts)}")
         for name, o in zip(("out[0]", "out[1]"), outs):
             _is_tensor(name, o)
     key = ("rotary", _sig(q), _sig(k), _sig(frequencies), _sig(positions), layout, amplitude, inverse,
@@ -226,16 +230,18 @@ def _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts,
 class _RotaryFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, rope, positions):
-        ctx.rope, ctx.positions = rope, positions
+        ctx.layout, ctx.amplitude = rope.layout, rope.amplitude
+        ctx.save_for_backward(rope.frequencies, positions)  # changed in place before the backward: refused by torch
         q, k = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (q, k))
         out = rotary(q, k, rope.frequencies, positions, rope.layout, rope.amplitude)
         return out if k is not None else out[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk=None):
-        rope = ctx.rope
+        frequencies, positions = ctx.saved_tensors
         dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
-        gq, gk = rotary(dq, dk, rope.frequencies, ctx.positions, rope.layout, rope.amplitude, inverse=True)
+        gq, gk = rotary(dq, dk, frequencies, positions, ctx.layout, ctx.amplitude, inverse=True)
         return gq, gk, None, None
 
 
@@ -261,7 +267,9 @@ def attention_mask(docs=None, prefix=None, causal: bool = True) -> AttentionMask
     some = docs if docs is not None else prefix
     if some is None:
         raise ValueError("attention_mask: docs or prefix needed (a plain causal mask needs none)")
-    _is_tensor("docs" if docs is not None else "prefix", some)
+    for name, t in (("docs", docs), ("prefix", prefix)):
+        if t is not None:
+            _is_tensor(name, t)
     key = ("mask", _sig(docs), _sig(prefix))
     nbytes = _plans.get(key)
     if nbytes is None:
@@ -291,8 +299,8 @@ class AttentionSaved(NamedTuple):
 
 def _dense_config(q, k, v, mask, causal, scale, softcap, slopes):
     _tensor("q", q)
-    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"q: shape {tuple(q.shape)} of {q.dtype}, expected [B, H, N, d] of bf16 or fp16")
+    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16) or q.shape[3] not in (64, 128) or not q.shape[1]:
+        raise ValueError(f"q: shape {tuple(q.shape)} of {q.dtype}, expected [B, H, N, 64 or 128] of bf16 or fp16")
     B, Hq, N, d = q.shape
     _tensor("k", k, q.device, q.dtype)
     if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d) or not k.shape[1] or Hq % k.shape[1]:
@@ -322,6 +330,7 @@ def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = Tru
     row sums from the rounded output, which costs accuracy where few keys carry a row."""
     for name, t in (("q", q), ("k", k), ("v", v)):
         _is_tensor(name, t)
+    scale, softcap, causal = None if scale is None else float(scale), float(softcap), bool(causal)
     key = ("dense_forward", _sig(q), _sig(k), _sig(v), None if mask is None else (mask.B, mask.N, _sig(mask.spans)),
            causal, scale, softcap, _sig(slopes))
     plan = _plans.get(key)
@@ -334,6 +343,8 @@ def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = Tru
     o = torch.empty_strided(q.shape, o_stride, dtype=q.dtype, device=q.device)
     lse = torch.empty(rows, dtype=torch.float32, device=q.device)
     low = torch.empty(q.shape, dtype=q.dtype, device=q.device) if for_backward else None
+    if lse.numel() == 0:
+        return o, AttentionSaved(lse, low)
     index = q.device.index
     _call("lh_dense_fwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           None if mask is None else mask.spans.data_ptr(), _ptr(slopes), o.data_ptr(), _ptr(low), lse.data_ptr(),
@@ -347,6 +358,7 @@ def dense_backward(do, q, k, v, o, saved: AttentionSaved, mask: AttentionMask | 
     lse, low = saved
     for name, t in (("do", do), ("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse)):
         _is_tensor(name, t)
+    scale, softcap, causal = None if scale is None else float(scale), float(softcap), bool(causal)
     key = ("dense_backward", _sig(do), _sig(q), _sig(k), _sig(v), _sig(o), _sig(lse), _sig(low),
            None if mask is None else (mask.B, mask.N, _sig(mask.spans)), causal, scale, softcap, _sig(slopes))
     plan = _plans.get(key)
@@ -366,6 +378,8 @@ def dense_backward(do, q, k, v, o, saved: AttentionSaved, mask: AttentionMask | 
     cfg, strides = plan
     dq, dk, dv = (torch.empty_strided(t.shape, s, dtype=t.dtype, device=t.device)
                   for t, s in zip((q, k, v), strides))
+    if lse.numel() == 0:
+        return dq, dk, dv
     delta = torch.empty_like(lse)
     index = q.device.index
     _call("lh_dense_bwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(low),
@@ -388,27 +402,34 @@ def _usable(t):
 
 class _DenseAttentionFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, slopes, mask, opt):
+    def forward(ctx, q, k, v, slopes, mask, for_backward, opt):
         q, k, v = _usable(q), _usable(k), _usable(v)
-        o, saved = dense_forward(q, k, v, mask, slopes=slopes, for_backward=any(ctx.needs_input_grad[:3]), **opt)
-        ctx.save_for_backward(q, k, v, o, *saved)
-        ctx.slopes, ctx.mask, ctx.opt = slopes, mask, opt
+        o, saved = dense_forward(q, k, v, mask, slopes=slopes, for_backward=for_backward, **opt)
+        ctx.save_for_backward(q, k, v, o, *saved, slopes, None if mask is None else mask.spans)
+        ctx.mask, ctx.opt = mask, opt
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
-        q, k, v, o, lse, low = ctx.saved_tensors
-        dq, dk, dv = dense_backward(_usable(do), q, k, v, o, AttentionSaved(lse, low), ctx.mask, slopes=ctx.slopes,
+        q, k, v, o, lse, low, slopes, _ = ctx.saved_tensors
+        dq, dk, dv = dense_backward(_usable(do), q, k, v, o, AttentionSaved(lse, low), ctx.mask, slopes=slopes,
                                     **ctx.opt)
-        return dq, dk, dv, None, None, None
+        return dq, dk, dv, None, None, None, None
 
 
 def dense_attention(q, k, v, mask: AttentionMask | None = None, causal: bool = True, scale: float | None = None,
                     softcap: float = 0.0, slopes=None, rotary: Rotary | None = None, positions=None):
     """Masked attention with its gradient in q, k and v (arguments as dense_forward).  rotary: positions are applied
-    to q and k first."""
+    to q and k first.
+
+    Forward and backward may be captured in a CUDA graph.  While an eager graph of the same leaves is alive, capture
+    over other ones (`q.detach().requires_grad_()`): torch makes a leaf's accumulation wait on the stream that it was
+    first used on, which a capture does not allow."""
     if slopes is not None and slopes.requires_grad:
         raise ValueError("slopes: no gradient is computed for them")
     if rotary is not None:
         q, k = apply_rotary(q, k, rotary, positions)
-    return _DenseAttentionFn.apply(q, k, v, slopes, mask, dict(causal=causal, scale=scale, softcap=softcap))
+    for_backward = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))
+    return _DenseAttentionFn.apply(q, k, v, slopes, mask, for_backward,
+                                   dict(causal=causal, scale=scale, softcap=softcap))
