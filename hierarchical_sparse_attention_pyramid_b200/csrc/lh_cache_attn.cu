@@ -538,78 +538,76 @@ __device__ __forceinline__ int block_of(int64_t u, int64_t total, int blocks) {
   return (int)(((u + 1) * blocks + total - 1) / total - 1);
 }
 
-// row r of a tile whose pieces the blocks [c0, c1] have, into row `out` of the output
-template <int D, bool F16, int W>
-__device__ __forceinline__ void join_row(const CacheAttnArgs& a, int rows_per_tile, int c0, int c1, int r, int64_t out,
-                                         float (*sO)[D], float* sL, float* sM) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Row r of a tile whose pieces the blocks [c0, c1] have, by L lanes, or by all
+// PARTS * L threads of the block, each L of them a share of the pieces: a
+// share's outputs (lane's groups of 4 channels) and its sum of exponentials.
+template <int D, int L, int PARTS>
+__device__ __forceinline__ float join_row(const CacheAttnArgs& a, int rows_per_tile, int c0, int c1, int r, bool live,
+                                          float* sM, float4 (&o)[D / L / 4]) {
+  const int part = PARTS == 1 ? 0 : threadIdx.x / L, lane = threadIdx.x % L;
   auto place = [&](int c) { return ((int64_t)c * 2 + (c == c0)) * rows_per_tile + r; };
+  if (!live) c1 = c0 - 1;
   float mm = -INFINITY;
-  for (int c = c0 + (W == 1 ? lane : (int)threadIdx.x); c <= c1; c += W * 32) mm = fmaxf(mm, a.part_ml[place(c)].x);
+  for (int c = c0 + part * L + lane; c <= c1; c += PARTS * L) mm = fmaxf(mm, a.part_ml[place(c)].x);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-  if constexpr (W > 1) {
-    if (lane == 0) sM[warp] = mm;
+  for (int d = L / 2; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+  if constexpr (PARTS > 1) {
+    if (lane == 0) sM[part] = mm;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < W; ++w) mm = fmaxf(mm, sM[w]);
+    for (int w = 0; w < PARTS; ++w) mm = fmaxf(mm, sM[w]);
   }
   const float ref = mm == -INFINITY ? 0.f : mm;
-  constexpr int C = D / 32;
-  float o[C] = {}, sum = 0.f;
-#pragma unroll 8
-  for (int c = c0 + (W == 1 ? 0 : warp); c <= c1; c += W) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / L / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(PARTS == 1 ? 2 : 8)
+  for (int c = c0 + part; c <= c1; c += PARTS) {
     const float2 x = a.part_ml[place(c)];
     const float f = sm100::fast_exp2(x.x - ref);
     sum = fmaf(f, x.y, sum);
-    const float* po = a.part_o + place(c) * D + lane * C;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + place(c) * D) + lane;
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = fmaf(f, po[i], o[i]);
-  }
-  if constexpr (W > 1) {
-#pragma unroll
-    for (int i = 0; i < C; ++i) sO[warp][lane * C + i] = o[i];
-    if (lane == 0) sL[warp] = sum;
-    __syncthreads();
-    if (warp > 0) return;
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      sum += sL[w];
-#pragma unroll
-      for (int i = 0; i < C; ++i) o[i] += sO[w][lane * C + i];
+    for (int i = 0; i < D / L / 4; ++i) {
+      const float4 p = po[i * L];
+      o[i] = make_float4(fmaf(f, p.x, o[i].x), fmaf(f, p.y, o[i].y), fmaf(f, p.z, o[i].z), fmaf(f, p.w, o[i].w));
     }
   }
+  return sum;
+}
+template <int D, bool F16, int L>
+__device__ __forceinline__ void store_joined(const CacheAttnArgs& a, int64_t out, float sum, const float4 (&o)[D / L / 4]) {
   const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o) + (out * D + lane * C) / 2;
+  uint2* dst = reinterpret_cast<uint2*>(a.o) + out * (D / 4) + threadIdx.x % L;
 #pragma unroll
-  for (int i = 0; i < C; i += 2) dst[i / 2] = pack2<F16>(o[i] * inv, o[i + 1] * inv);
+  for (int i = 0; i < D / L / 4; ++i)
+    dst[i * L] = make_uint2(pack2<F16>(o[i].x * inv, o[i].y * inv), pack2<F16>(o[i].z * inv, o[i].w * inv));
 }
 
 // Joins the pieces of the query rows that lie in several blocks.
 //
-// Rows in few pieces (W = 1): blocks (x, ..) take the rows of the one
-// (sequence, head, row tile) that block x of the work began and did not finish,
-// if there is one, a warp a row at a time.  The work then goes by the blocks and
-// not by the rows of the call, most of which one block has whole: 4096
-// sequences, 32 query heads: 19 us, and 1.3 ms with a warp for every row.
-// Rows in many pieces, of which there are few (W = 8): block (i, r) takes row r
-// of the i-th (sequence, head, row tile); its warps share the pieces out and are
-// joined in warp order.  One sequence of 512K tokens: 7 us, 18 us by blocks.
-constexpr int kJoinWarps = 8;
-template <int D, bool F16, int W>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+// Rows in few pieces: blocks (x, ..) take the rows of the one (sequence, head,
+// row tile) that block x of the work began and did not finish, if there is one,
+// L lanes a row.  The work then goes by the blocks and not by the rows of the
+// call, most of which one block has whole: 4096 sequences, 32 query heads:
+// 19 us, and 1.3 ms with a warp for every row.
+// MANY pieces a row, and few rows: block (i, r) takes row r of the i-th
+// (sequence, head, row tile); L threads each take a share of its pieces, and the
+// shares are joined in their order.  One sequence of 512K tokens: 7 us, 18 us by
+// blocks.
+constexpr int kJoinThreads = 256;
+template <int D, bool F16, bool MANY, int L>
+__global__ void __launch_bounds__(kJoinThreads)
     cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a, int rows_per_tile) {
-  __shared__ float sO[W == 1 ? 1 : W][D];
-  __shared__ float sL[kJoinWarps], sM[kJoinWarps];
-  __shared__ int64_t scan[kJoinWarps + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.Hq / a.c.heads;
+  constexpr int PARTS = MANY ? kJoinThreads / L : 1;
+  __shared__ float4 sO[PARTS][MANY ? L : 1];
+  __shared__ float sL[PARTS], sM[PARTS];
+  __shared__ int64_t scan[kJoinThreads / 32 + 1];
+  const int lane = threadIdx.x & 31, G = a.Hq / a.c.heads;
   Seq seq{0, 0, 0};
   int hk = 0, rt = 0, c0 = 0, c1 = 0;
-  if constexpr (W == 1) {
-    const Stretch st = find_stretch<kJoinWarps, true>(a, rows_per_tile, scan);
+  if constexpr (!MANY) {
+    const Stretch st = find_stretch<kJoinThreads / 32, true>(a, rows_per_tile, scan);
     if (st.u < st.u_end) {
       seq = load_seq(a, st.s, false);
       const int kt_n = key_units(seq.len), tiles = (seq.T * G + rows_per_tile - 1) / rows_per_tile;
@@ -647,13 +645,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
   cudaGridDependencySynchronize();  // every block: what follows in the stream waits for this kernel alone
   if (c0 == c1) return;             // written by that block
-#pragma unroll 1
-  for (int r = W == 1 ? blockIdx.y * kJoinWarps + warp : blockIdx.y; r < rows_per_tile; r += gridDim.y * (kJoinWarps / W)) {
-    const int row = rt * rows_per_tile + r;
-    if (row >= seq.T * G) break;
-    join_row<D, F16, W>(a, rows_per_tile, c0, c1, r, (int64_t)(seq.tok0 + row / G) * a.Hq + hk * G + row % G, sO, sL,
-                        sM);
+  const int r = MANY ? blockIdx.y : (blockIdx.y * kJoinThreads + threadIdx.x) / L;
+  const int row = rt * rows_per_tile + r;
+  const bool live = r < rows_per_tile && row < seq.T * G;
+  float4 o[D / L / 4];
+  float sum = join_row<D, L, PARTS>(a, rows_per_tile, c0, c1, r, live, sM, o);
+  if constexpr (MANY) {
+    static_assert(D == 4 * L, "a group of channels a lane");
+    const int part = threadIdx.x / L, at = threadIdx.x % L;
+    sO[part][at] = o[0];
+    if (at == 0) sL[part] = sum;
+    __syncthreads();
+    if (part > 0) return;
+    sum = 0.f;
+    o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < PARTS; ++w) {
+      const float4 p = sO[w][at];
+      sum += sL[w];
+      o[0] = make_float4(o[0].x + p.x, o[0].y + p.y, o[0].z + p.z, o[0].w + p.w);
+    }
   }
+  if (live)
+    store_joined<D, F16, L>(a, (int64_t)(seq.tok0 + row / G) * a.Hq + hk * G + row % G, sum, o);
 }
 
 template <int D, int KIND, bool F16, int NB>
@@ -690,18 +704,18 @@ cudaError_t join(const CacheAttnArgs& a, int rows_per_tile, cudaStream_t st) {
   const bool many = a.blocks >= 8 * tiles;  // pieces of a row
   // it may be brought up while the pieces run; it waits for them itself
   cudaLaunchConfig_t cfg{};
-  // W = 1: up to 4 rows a warp, so that finding the place in the work list is shared
   cfg.gridDim = many ? dim3((unsigned)tiles, (unsigned)rows_per_tile)
-                     : dim3((unsigned)a.blocks, (unsigned)(rows_per_tile <= 4 * kJoinWarps ? rows_per_tile / kJoinWarps : 4));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+                     : dim3((unsigned)a.blocks, (unsigned)((rows_per_tile + 31) / 32));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 8>, a, rows_per_tile)
-              : cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, 1>, a, rows_per_tile);
+  if (many) return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, true, D / 4>, a, rows_per_tile);
+  if (rows_per_tile == 8) return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, false, D / 4>, a, rows_per_tile);
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, F16, false, 8>, a, rows_per_tile);
 }
 
 }  // namespace
