@@ -24,22 +24,19 @@ class KVCache:
     stay the ones it was made of: the library holds their addresses."""
 
     def __setattr__(self, name, value):
-        if "ref" in self.__dict__:
-            raise AttributeError(f"{name}: a KVCache is made anew for other tensors")
-        super().__setattr__(name, value)
+        raise AttributeError(f"{name}: a KVCache is made anew for other tensors")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _is_tensor("k", k)
-        self.sig = ("cache", _sig(k), _sig(v), _sig(k_scale), _sig(v_scale))
-        plan = _plans.get(self.sig)
+        sig = ("cache", _sig(k), _sig(v), _sig(k_scale), _sig(v_scale))
+        plan = _plans.get(sig)
         if plan is None:
-            plan = _keep(self.sig, self._check(k, v, k_scale, v_scale))
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.heads, self.page, self.d, self.kind = plan
-        self.device = k.device
-        self.c = LhCache(self.pages, self.page, self.heads, self.d, _lib.CACHE_KINDS[self.kind], k.data_ptr(),
-                         v.data_ptr(), _ptr(k_scale), _ptr(v_scale))
-        self.ref = ctypes.byref(self.c)
+            plan = _keep(sig, self._check(k, v, k_scale, v_scale))
+        pages, heads, page, d, kind = plan
+        c = LhCache(pages, page, heads, d, _lib.CACHE_KINDS[kind], k.data_ptr(), v.data_ptr(), _ptr(k_scale),
+                    _ptr(v_scale))
+        self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, sig=sig, pages=pages, heads=heads, page=page,
+                             d=d, kind=kind, device=k.device, c=c, ref=ctypes.byref(c))
 
     @staticmethod
     def _check(k, v, k_scale, v_scale):
@@ -113,11 +110,12 @@ def cache_read(cache: KVCache, page_table, starts, total: int, dtype=torch.bfloa
             raise ValueError(f"total: {total}, expected 0 or more")
         if dtype not in _NAMES:
             raise ValueError(f"dtype: {dtype}, expected bf16, fp16 or fp32")
-        plan = _keep(key, (seqs, width, _lib.DENSE_DTYPES[_NAMES[dtype]], (total, cache.heads, cache.d)))
-    seqs, width, code, shape = plan
+        plan = _keep(key, (seqs, width, _lib.DENSE_DTYPES[_NAMES[dtype]], (total, cache.heads, cache.d),
+                           (cache.heads * cache.d, cache.d, 1)))
+    seqs, width, code, shape, strides = plan
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=cache.device),
-               torch.empty(shape, dtype=dtype, device=cache.device))
+        out = (torch.empty_strided(shape, strides, dtype=dtype, device=cache.device),
+               torch.empty_strided(shape, strides, dtype=dtype, device=cache.device))
     else:
         for name, t in zip(("out[0]", "out[1]"), out):
             _flat(name, t, cache.device, dtype, shape)
@@ -147,7 +145,7 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
         plan = _keep(key, (cfg, _lib.load().lh_cache_attn_ws_bytes(cache.ref, cfg)))
     cfg, need = plan
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _flat("out", out, q.device, q.dtype, q.shape)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None

@@ -188,7 +188,7 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
         for name, o in zip(("out[0]", "out[1]"), outs):
             _is_tensor(name, o)
     key = ("rotary", _sig(q), _sig(k), _sig(frequencies), _sig(positions), layout, amplitude, inverse,
-           *((o.shape, o.stride(), o.dtype, o.device) for o in outs))
+           None if out is None else tuple(_sig(o) for o in outs))
     cfg = _plans.get(key)
     if cfg is None:
         cfg = _keep(key, _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs))
@@ -338,12 +338,13 @@ def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = Tru
         cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
         o = _like(q)
         cfg.o_stride = _strides(o)
-        plan = _keep(key, (ctypes.byref(cfg), q.shape[:3], o.stride()))
-    cfg, rows, o_stride = plan
-    o = torch.empty_strided(q.shape, o_stride, dtype=q.dtype, device=q.device)
-    lse = torch.empty(rows, dtype=torch.float32, device=q.device)
-    low = torch.empty(q.shape, dtype=q.dtype, device=q.device) if for_backward else None
-    if lse.numel() == 0:
+        B, Hq, N, d = q.shape
+        plan = _keep(key, (ctypes.byref(cfg), (*q.shape,), o.stride(), (B, Hq, N), (Hq * N, N, 1)))
+    cfg, shape, o_stride, rows, rows_stride = plan
+    o = torch.empty_strided(shape, o_stride, dtype=q.dtype, device=q.device)
+    lse = torch.empty_strided(rows, rows_stride, dtype=torch.float32, device=q.device)
+    low = torch.empty_like(q, memory_format=torch.contiguous_format) if for_backward else None
+    if not rows[0] or not rows[2]:
         return o, AttentionSaved(lse, low)
     index = q.device.index
     _call("lh_dense_fwd", index, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(),
