@@ -13,7 +13,8 @@ import torch
 
 from . import _lib
 from ._lib import LhCache, LhCacheAttnConfig
-from .dense import _NAMES, _call, _err, _flat, _is_tensor, _keep, _plans, _ptr, _sig, _tensor
+from .dense import (_NAMES, _are_tensors, _call, _contiguous_like, _err, _flat, _is_tensor, _keep, _not_tensors, _plans, _ptr, _sig,
+                    _tensor)
 
 _KINDS = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float8_e4m3fn: "e4m3", torch.int8: "int8"}
 
@@ -72,11 +73,14 @@ def _table(cache: KVCache, page_table):
 def cache_write(cache: KVCache, k, v, slots) -> None:
     """Write tokens k, v [n, heads, d] (bf16, fp16 or fp32, channels contiguous) at slots (int64 [n]: page id * page +
     row; negative: skipped), quantised as the cache holds them.  A slot may be given once in a call."""
-    for name, t in (("k", k), ("v", v), ("slots", slots)):
-        _is_tensor(name, t)
-    key = ("cache_write", cache.sig, _sig(k), _sig(v), _sig(slots))
+    try:
+        key = ("cache_write", cache.sig, _sig(k), _sig(v), _sig(slots))
+    except AttributeError:
+        _not_tensors(k=k, v=v, slots=slots)
+        raise
     plan = _plans.get(key)
     if plan is None:
+        _are_tensors(k=k, v=v, slots=slots)
         _tensor("k", k, cache.device)
         if k.dim() != 3 or tuple(k.shape[1:]) != (cache.heads, cache.d) or k.dtype not in _NAMES:
             raise ValueError(f"k: shape {tuple(k.shape)} of {k.dtype}, expected [n, {cache.heads}, {cache.d}] of bf16, "
@@ -98,12 +102,15 @@ def cache_read(cache: KVCache, page_table, starts, total: int, dtype=torch.bfloa
     """The first starts[s+1] - starts[s] tokens of every sequence s, by its row of page_table (int32 [sequences,
     pages]), in rows starts[s] .. of (k, v) [total, heads, d].  out: (k, v) to write; rows of no sequence are left as
     they are (uninitialised without out)."""
-    for name, t in (("page_table", page_table), ("starts", starts)):
-        _is_tensor(name, t)
     total = operator.index(total)
-    key = ("cache_read", cache.sig, _sig(page_table), _sig(starts), total, dtype)
+    try:
+        key = ("cache_read", cache.sig, _sig(page_table), _sig(starts), total, dtype)
+    except AttributeError:
+        _not_tensors(page_table=page_table, starts=starts)
+        raise
     plan = _plans.get(key)
     if plan is None:
+        _are_tensors(page_table=page_table, starts=starts)
         seqs, width = _table(cache, page_table)
         _flat("starts", starts, cache.device, torch.int32, (seqs + 1,))
         if total < 0:
@@ -134,18 +141,21 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
     [sequences + 1], first query token of each sequence, at most max_tokens each; None: one each.  A token sees the
     positions up to its own; with tree_mask (int64 [n]) all positions before the sequence's query tokens, and query
     token u of its sequence where bit u is set.  scale, softcap, slopes: as dense_forward."""
-    for name, t in (("q", q), ("page_table", page_table), ("lens", lens)):
-        _is_tensor(name, t)
     scale, softcap, max_tokens = None if scale is None else float(scale), float(softcap), operator.index(max_tokens)
-    key = ("cache_attention", cache.sig, _sig(q), _sig(page_table), _sig(lens), _sig(q_start), max_tokens,
-           _sig(tree_mask), scale, softcap, _sig(slopes))
+    try:
+        key = ("cache_attention", cache.sig, _sig(q), _sig(page_table), _sig(lens), _sig(q_start), max_tokens,
+               _sig(tree_mask), scale, softcap, _sig(slopes))
+    except AttributeError:
+        _not_tensors(q=q, page_table=page_table, lens=lens, q_start=q_start, tree_mask=tree_mask, slopes=slopes)
+        raise
     plan = _plans.get(key)
     if plan is None:
+        _are_tensors(q=q, page_table=page_table, lens=lens)
         cfg = _attention_config(cache, q, page_table, lens, q_start, max_tokens, tree_mask, scale, softcap, slopes)
         plan = _keep(key, (cfg, _lib.load().lh_cache_attn_ws_bytes(cache.ref, cfg)))
     cfg, need = plan
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _contiguous_like(q)
     else:
         _flat("out", out, q.device, q.dtype, q.shape)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None

@@ -117,6 +117,7 @@ struct Strides {
 
 struct DenseArgs {
   int B, N, Hq, Hkv, n_tiles;
+  int q_per_cta;    // the forward's query tiles of a CTA, 1 or 2
   float scale;      // of the scores
   float softcap;    // 0: none
   const float* slopes;  // [Hq] or NULL

@@ -3,7 +3,7 @@
 // key head h / (Hq / Hkv)).
 //
 // One pass over the keys with a running maximum and sum per query row.  One
-// CTA owns two 128-query tiles (A, B) of one head and streams the key tiles
+// CTA owns two 128-query tiles (A, B; small calls: A alone) of one head and streams the key tiles
 // of both through a 2-stage ring; while one tile's softmax runs, the tensor
 // core works on the other's products.
 //   warps 0-3, 4-7  softmax of tile A, B: thread t owns query row t (TMEM
@@ -72,19 +72,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // pair-major grid, last pairs first: causal rows are longest there, and the
   // short ones fill the tail
-  const int n_pairs = (a.n_tiles + 1) / 2;
+  const int n_ctas = (a.n_tiles + a.q_per_cta - 1) / a.q_per_cta;  // of a head
   const int BH = a.B * a.Hq;
-  const int c = n_pairs - 1 - (int)(blockIdx.x / (unsigned)BH);
+  const int qt = (n_ctas - 1 - (int)(blockIdx.x / (unsigned)BH)) * a.q_per_cta;  // first query tile
   const int bh = (int)(blockIdx.x % (unsigned)BH);
   const int b = bh / a.Hq, h = bh % a.Hq, hk = h / (a.Hq / a.Hkv);
-  const bool hasB = 2 * c + 1 < a.n_tiles;
+  const bool hasB = a.q_per_cta == 2 && qt + 1 < a.n_tiles;
   // key tiles [first, end) of each query tile, and of both
   TileSpan span[2];
   int first[2], end[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     span[x] = {0, 0, 0, 0};
-    if (x == 0 || hasB) span[x] = mask_row_tile(a.mask, b, 2 * c + x, a.N);
+    if (x == 0 || hasB) span[x] = mask_row_tile(a.mask, b, qt + x, a.N);
     first[x] = span[x].min_lo >> 7;
     end[x] = span[x].max_hi > span[x].min_lo ? (span[x].max_hi + 127) >> 7 : first[x];
   }
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_expect_tx(bQ, (hasB ? 2 : 1) * 128 * D * 2);
       for (int x = 0; x < (hasB ? 2 : 1); ++x)
         for (int ch = 0; ch < D / 64; ++ch)
-          tma_load_4d(smem + Lay::oQ + x * Lay::kTile + ch * kRegion, &tmQ, bQ, ch * 64, (2 * c + x) * 128, h, b);
+          tma_load_4d(smem + Lay::oQ + x * Lay::kTile + ch * kRegion, &tmQ, bQ, ch * 64, (qt + x) * 128, h, b);
       for (int j = j0; j < j1; ++j) {
         const int i = j - j0, st = i & 1, use = i >> 1;
         if (i >= 2 && !mbar_wait(&bKVfree[st], (use - 1) & 1, abort_flag)) break;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp >> 2;
     const int j_first = x ? first[1] : first[0], j_end = x ? end[1] : end[0];
     const TileSpan sp = x ? span[1] : span[0];
-    const int row = (2 * c + x) * 128 + (warp & 3) * 32 + lane;
+    const int row = (qt + x) * 128 + (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = tl + x * 128, to = tl + 256 + x * D;
     const int2 keys = mask_row(a.mask, b, row, a.N);
@@ -388,9 +388,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool F16, bool MOD>
-cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const DenseArgs& a, void* o,
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, DenseArgs a, void* o,
                    const Strides& so, void* o_low, cudaStream_t st) {
-  const int64_t grid = (int64_t)((a.n_tiles + 1) / 2) * a.B * a.Hq;
+  // one query tile a CTA where the GPU takes all of them at once: two share the
+  // CTA's issue slots and its ring (1024 tokens, 16 heads of 128: 20 us, 24 in
+  // pairs; 4096 tokens, 4 heads: 58, 67)
+  a.q_per_cta = (int64_t)a.n_tiles * a.B * a.Hq <= 148 ? 1 : 2;
+  const int64_t grid = (int64_t)((a.n_tiles + a.q_per_cta - 1) / a.q_per_cta) * a.B * a.Hq;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   auto* fn = dense_fwd_kernel<D, F16, MOD>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);

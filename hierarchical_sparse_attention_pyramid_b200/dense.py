@@ -103,6 +103,16 @@ def _is_tensor(name: str, t):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
 
 
+def _are_tensors(**ts):
+    for name, t in ts.items():
+        _is_tensor(name, t)
+
+
+def _not_tensors(**ts):
+    """The error for arguments (None: not given) that a call's key could not be made of."""
+    _are_tensors(**{name: t for name, t in ts.items() if t is not None})
+
+
 def _flat(name: str, t, device, dtype, shape):
     _tensor(name, t, device, dtype, shape)
     if not t.is_contiguous():
@@ -175,20 +185,17 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
     (2i, 2i + 1) with "interleaved".  positions: int32 [B, N], or None for 0 .. N-1.  inverse turns back: the
     gradient of a call is the inverse call on the output's gradient.  out: (q', k') to write, which may be (q, k)."""
     ts = (q,) if k is None else (q, k)
-    for name, t in zip(("q", "k"), ts):
-        _is_tensor(name, t)
-    _is_tensor("frequencies", frequencies)
     amplitude, inverse = float(amplitude), bool(inverse)
-    if out is None:
-        outs = [torch.empty_like(t) for t in ts]
-    else:
-        outs = list(out)[:len(ts)]
-        if len(outs) < len(ts):
-            raise ValueError(f"out: {len(outs)} tensors, expected {len(ts)}")
-        for name, o in zip(("out[0]", "out[1]"), outs):
-            _is_tensor(name, o)
-    key = ("rotary", _sig(q), _sig(k), _sig(frequencies), _sig(positions), layout, amplitude, inverse,
-           None if out is None else tuple(_sig(o) for o in outs))
+    try:
+        outs = [torch.empty_like(t) for t in ts] if out is None else list(out)[:len(ts)]
+        key = ("rotary", _sig(q), _sig(k), _sig(frequencies), _sig(positions), layout, amplitude, inverse,
+               None if out is None else tuple(_sig(o) for o in outs))
+    except (AttributeError, TypeError):
+        _are_tensors(q=q, frequencies=frequencies)
+        _not_tensors(k=k, positions=positions)
+        raise
+    if len(outs) < len(ts):
+        raise ValueError(f"out: {len(outs)} tensors, expected {len(ts)}")
     cfg = _plans.get(key)
     if cfg is None:
         cfg = _keep(key, _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs))
@@ -199,6 +206,7 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
 
 
 def _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs):
+    _are_tensors(q=q, frequencies=frequencies)
     _tensor("q", q)
     if q.dim() != 4 or q.dtype not in _NAMES:
         raise ValueError(f"q: shape {tuple(q.shape)} of {q.dtype}, expected [B, H, N, d] of bf16, fp16 or fp32")
@@ -252,8 +260,7 @@ def apply_rotary(q, k, rope: Rotary, positions=None):
 
 # ------------------------------------------------------------------ masks
 
-@dataclass(frozen=True)
-class AttentionMask:
+class AttentionMask(NamedTuple):
     """A mask of the dense attention over B rows of N tokens; attention_mask makes it, every layer shares it."""
     B: int
     N: int
@@ -267,10 +274,11 @@ def attention_mask(docs=None, prefix=None, causal: bool = True) -> AttentionMask
     some = docs if docs is not None else prefix
     if some is None:
         raise ValueError("attention_mask: docs or prefix needed (a plain causal mask needs none)")
-    for name, t in (("docs", docs), ("prefix", prefix)):
-        if t is not None:
-            _is_tensor(name, t)
-    key = ("mask", _sig(docs), _sig(prefix))
+    try:
+        key = ("mask", _sig(docs), _sig(prefix))
+    except AttributeError:
+        _not_tensors(docs=docs, prefix=prefix)
+        raise
     nbytes = _plans.get(key)
     if nbytes is None:
         _tensor("docs" if docs is not None else "prefix", some)
@@ -328,22 +336,25 @@ def dense_forward(q, k, v, mask: AttentionMask | None = None, causal: bool = Tru
     softcap > 0: scores x become softcap * tanh(x / softcap).  slopes: fp32 [Hq], scores get -slope |i - j|.
     A query without keys gets o = 0, lse = -inf.  for_backward False leaves o_low out: dense_backward then takes its
     row sums from the rounded output, which costs accuracy where few keys carry a row."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _is_tensor(name, t)
     scale, softcap, causal = None if scale is None else float(scale), float(softcap), bool(causal)
-    key = ("dense_forward", _sig(q), _sig(k), _sig(v), None if mask is None else (mask.B, mask.N, _sig(mask.spans)),
-           causal, scale, softcap, _sig(slopes))
+    try:
+        key = ("dense_forward", _sig(q), _sig(k), _sig(v), None if mask is None else (mask.B, mask.N, _sig(mask.spans)),
+               causal, scale, softcap, _sig(slopes))
+    except AttributeError:
+        _not_tensors(q=q, k=k, v=v, slopes=slopes)
+        raise
     plan = _plans.get(key)
     if plan is None:
+        _are_tensors(q=q, k=k, v=v)
         cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
-        o = _like(q)
-        cfg.o_stride = _strides(o)
+        make_o = _maker(q)
+        cfg.o_stride = _strides(make_o(q))
         B, Hq, N, d = q.shape
-        plan = _keep(key, (ctypes.byref(cfg), (*q.shape,), o.stride(), (B, Hq, N), (Hq * N, N, 1)))
-    cfg, shape, o_stride, rows, rows_stride = plan
-    o = torch.empty_strided(shape, o_stride, dtype=q.dtype, device=q.device)
+        plan = _keep(key, (ctypes.byref(cfg), make_o, (B, Hq, N), (Hq * N, N, 1)))
+    cfg, make_o, rows, rows_stride = plan
+    o = make_o(q)
     lse = torch.empty_strided(rows, rows_stride, dtype=torch.float32, device=q.device)
-    low = torch.empty_like(q, memory_format=torch.contiguous_format) if for_backward else None
+    low = _contiguous_like(q) if for_backward else None
     if not rows[0] or not rows[2]:
         return o, AttentionSaved(lse, low)
     index = q.device.index
@@ -357,13 +368,16 @@ def dense_backward(do, q, k, v, o, saved: AttentionSaved, mask: AttentionMask | 
                    scale: float | None = None, softcap: float = 0.0, slopes=None):
     """Gradients of dense_forward's o with its inputs and both of its results -> (dq, dk, dv)."""
     lse, low = saved
-    for name, t in (("do", do), ("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse)):
-        _is_tensor(name, t)
     scale, softcap, causal = None if scale is None else float(scale), float(softcap), bool(causal)
-    key = ("dense_backward", _sig(do), _sig(q), _sig(k), _sig(v), _sig(o), _sig(lse), _sig(low),
-           None if mask is None else (mask.B, mask.N, _sig(mask.spans)), causal, scale, softcap, _sig(slopes))
+    try:
+        key = ("dense_backward", _sig(do), _sig(q), _sig(k), _sig(v), _sig(o), _sig(lse), _sig(low),
+               None if mask is None else (mask.B, mask.N, _sig(mask.spans)), causal, scale, softcap, _sig(slopes))
+    except AttributeError:
+        _not_tensors(do=do, q=q, k=k, v=v, o=o, lse=lse, o_low=low, slopes=slopes)
+        raise
     plan = _plans.get(key)
     if plan is None:
+        _are_tensors(do=do, q=q, k=k, v=v, o=o, lse=lse)
         cfg = _dense_config(q, k, v, mask, causal, scale, softcap, slopes)
         for name, t in (("do", do), ("o", o)):
             _tensor(name, t, q.device, q.dtype, q.shape)
@@ -372,13 +386,12 @@ def dense_backward(do, q, k, v, o, saved: AttentionSaved, mask: AttentionMask | 
         _flat("lse", lse, q.device, torch.float32, q.shape[:3])
         if low is not None:
             _flat("o_low", low, q.device, q.dtype, q.shape)
-        grads = [_like(t) for t in (q, k, v)]
+        make = [_maker(t) for t in (q, k, v)]
         cfg.o_stride, cfg.do_stride = _strides(o), _strides(do)
-        cfg.dq_stride, cfg.dk_stride, cfg.dv_stride = (_strides(g) for g in grads)
-        plan = _keep(key, (ctypes.byref(cfg), [g.stride() for g in grads]))
-    cfg, strides = plan
-    dq, dk, dv = (torch.empty_strided(t.shape, s, dtype=t.dtype, device=t.device)
-                  for t, s in zip((q, k, v), strides))
+        cfg.dq_stride, cfg.dk_stride, cfg.dv_stride = (_strides(m(t)) for m, t in zip(make, (q, k, v)))
+        plan = _keep(key, (ctypes.byref(cfg), *make))
+    cfg, make_q, make_k, make_v = plan
+    dq, dk, dv = make_q(q), make_k(k), make_v(v)
     if lse.numel() == 0:
         return dq, dk, dv
     delta = torch.empty_like(lse)
@@ -389,10 +402,13 @@ def dense_backward(do, q, k, v, o, saved: AttentionSaved, mask: AttentionMask | 
     return dq, dk, dv
 
 
-def _like(t):
-    """An output like t: with its strides where the kernels can write them."""
-    o = torch.empty_like(t)
-    return o if _addressable(o) else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _contiguous_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _maker(t):
+    """What allocates an output like t: with its strides where the kernels can write them."""
+    return torch.empty_like if _addressable(torch.empty_like(t)) else _contiguous_like
 
 
 def _usable(t):
