@@ -9,7 +9,9 @@
 // stages of K and V go round a chain of latencies, from the conversion over the
 // scores and the softmax of a thread a row to the product that frees them.  Two
 // groups of softmax warps, of converters, or of both (96 registers a thread),
-// and K and V freed apart did not shorten it for 8-bit caches.
+// and K and V freed apart did not shorten it for 8-bit caches; rows staged by
+// asynchronous copies two units ahead, with two softmax groups, took 8% off at
+// 16 sequences x 8 heads and nothing at 4, and was not kept.
 //   warps 0-3   softmax: thread t owns row t (TMEM lane t) and all 128 keys of
 //               a unit; they write the Q tile at the start of a piece and the
 //               outputs at its end
