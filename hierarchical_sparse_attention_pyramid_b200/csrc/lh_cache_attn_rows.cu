@@ -4,11 +4,11 @@
 //
 // Each key is read and, where the cache holds 8 bits, turned into a 16-bit
 // operand once for all 128 rows.  A unit of 128 keys takes 1024 clocks of matrix
-// products at 128 channels but about 6000 in all (3.3 us; one sequence of 256K
-// e4m3 tokens, 4 key heads, 96 rows: 188 us against a floor of 42): its two
-// stages of K and V go round a chain of latencies, from the conversion over the
-// scores and the softmax of a thread a row to the product that frees them.  Two
-// groups of softmax warps, of converters, or of both (96 registers a thread),
+// products at 128 channels but about 5500 in all (3 us; one sequence of 256K
+// e4m3 tokens, 4 key heads, 96 rows: 188 us against a floor of 42): by the clock
+// the converters spend 3300 on a unit's loads and 1300 on its conversion, and a
+// softmax of a thread a row 4600, beside one another but in a chain over two
+// stages.  Two groups of softmax warps, of converters, or of both (96 registers a thread),
 // and K and V freed apart did not shorten it for 8-bit caches; rows staged by
 // asynchronous copies two units ahead, with two softmax groups, took 8% off at
 // 16 sequences x 8 heads and nothing at 4, and was not kept.

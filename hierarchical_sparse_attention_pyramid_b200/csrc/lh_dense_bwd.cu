@@ -25,6 +25,10 @@
 // keys (a column's queries), so that they stay below the rounding of the
 // gradients themselves.  The score scale is left out of dS and applied to the
 // fp32 sums: with fp16 that keeps small dS out of the subnormal range.
+//
+// Bound by the tensor cores: 16K causal tokens, 8 heads of 128: 623 us for dQ's
+// three products (1.32 PFLOP/s) and 843 us for the other four (1.30), near the
+// 1.37 that a long product of large matrices sustains under the power limit.
 #include <type_traits>
 
 #include "lh_dense.cuh"

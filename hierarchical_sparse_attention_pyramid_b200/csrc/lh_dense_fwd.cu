@@ -3,9 +3,11 @@
 // key head h / (Hq / Hkv)).
 //
 // One pass over the keys with a running maximum and sum per query row.  One
-// CTA owns two 128-query tiles (A, B; small calls: A alone) of one head and streams the key tiles
-// of both through a 2-stage ring; while one tile's softmax runs, the tensor
-// core works on the other's products.
+// CTA owns two 128-query tiles (A, B; small calls: A alone) of one head and
+// streams the key tiles of both through a 2-stage ring; while one tile's softmax
+// runs, the tensor core works on the other's products.  Bound by those two
+// together: 16K causal tokens, 8 heads of 128: 477 us (1.15 PFLOP/s; the tensor
+// cores busy for 59% of the time), with a cap or a distance bias by the softmax.
 //   warps 0-3, 4-7  softmax of tile A, B: thread t owns query row t (TMEM
 //                   lane t) and all 128 keys of a key tile
 //   warp 8          TMA producer
@@ -13,7 +15,7 @@
 //                   P_B V, the next S_B
 // TMEM columns: S_A/P_A [0,128), S_B/P_B [128,256), O_A [256,256+D),
 // O_B [256+D,256+2D).  P goes back over the first half of the 64 S columns it
-// came from, in the inputs' 16-bit type: its rounding (half a step, 2^-9 in bf16)
+// came from, in the inputs' 16-bit type: its rounding (half a step, 2^-8 in bf16)
 // is averaged over the row's keys and stays below the rounding of O itself.
 // The sums, the maximum, O and LSE are fp32; what O's rounding takes off can be
 // written too (O_low): the backward's Delta = rowsum(dO * O) cancels against dP,

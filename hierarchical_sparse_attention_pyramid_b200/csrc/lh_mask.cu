@@ -7,8 +7,8 @@
 // padding is.  The masks come from ballots over coalesced loads; what lies
 // before and after a thread's tokens comes from three block scans; the spans
 // then follow from the masks by bit operations, 32 tokens of one thread at a
-// time, again with coalesced stores.  Bound by latency: 8K tokens take a few
-// microseconds, once per batch (every layer and both directions share it).
+// time, again with coalesced stores.  Bound by latency: 8K tokens take
+// 13 us, 257 tokens 6, once per batch (every layer and both directions share it).
 #include "lh_common.cuh"
 #include "lh_dense.cuh"
 
