@@ -850,8 +850,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, bool F16, bool MOD>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& go,
-                   const DenseArgs& a, const void* o, const Strides& so, const void* o_low, const void* dout, const Strides& sdo, void* dq,
-                   const Strides& sdq, void* dk, const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st) {
+                   const DenseArgs& a, const void* o, const Strides& so, const void* o_low, const void* dout,
+                   const Strides& sdo, void* dq, const Strides& sdq, void* dk, const Strides& sdk, void* dv,
+                   const Strides& sdv, cudaStream_t st) {
   const int64_t gq = (int64_t)a.n_tiles * a.B * a.Hq, gk = (int64_t)a.n_tiles * a.B * a.Hkv;
   if (gq > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   auto* fq = dense_bwd_q_kernel<D, F16, MOD>;
@@ -888,8 +889,8 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
 
 cudaError_t launch_dense_bwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, const CUtensorMap& go, const void* o, const Strides& so,
-                             const void* o_low, const void* dout, const Strides& sdo, void* dq, const Strides& sdq, void* dk,
-                             const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st) {
+                             const void* o_low, const void* dout, const Strides& sdo, void* dq, const Strides& sdq,
+                             void* dk, const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st) {
   const bool mod = a.softcap > 0.f || a.slopes;
   auto pick = [&](auto D, auto F, auto M) {
     return launch<decltype(D)::value, decltype(F)::value, decltype(M)::value>(q, k, v, go, a, o, so, o_low, dout, sdo, dq,
