@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bDP = bars + 15;      // dP of the current key tile in TMEM
   uint64_t* bPS = bars + 16;      // dS written over the tile's S columns (256 arrivals)
   uint64_t* bDone = bars + 17;    // every product done
+  uint64_t* bDel = bars + 18;     // O and O_low read (256 arrivals)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::oBar + 192);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::oBar + 196);
 
@@ -527,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bDP, 1);
     mbar_init(bPS, kCompute);
     mbar_init(bDone, 1);
+    mbar_init(bDel, kCompute);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -553,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_expect_tx(&bK[sk], 128 * D * 2);
         for (int c = 0; c < D / 64; ++c)
           tma_load_4d(smem + Lay::oK + sk * Lay::kTile + c * kRegion, &tmK, &bK[sk], c * 64, (k0 + j) * 128, hk, b);
+        if (j == 1 && !mbar_wait(bDel, 0, abort_flag)) break;  // O and O_low are out of the last stages
         if (j >= 2 && !mbar_wait(&bVfree[sv], ((j >> 1) - 1) & 1, abort_flag)) break;
         mbar_expect_tx(&bV[sv], 128 * D * 2);
         for (int c = 0; c < D / 64; ++c)
@@ -636,36 +639,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = (warp & 3) * 32 + lane;  // query row of the tile (TMEM lane)
     const int q = qt * 128 + t;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    // Delta of the tile's rows, a warp 16 of them
+    // Delta of the tile's rows.  O and O_low come by asynchronous copies into the
+    // last K and V stages, which the producer fills after bDel (loads through the
+    // 28 KB that the kernel leaves the L1 cache took 12000 clocks a tile), dO
+    // is in shared memory for the product; each warpgroup sums half of the channels.
     float* sDel = reinterpret_cast<float*>(smem + Lay::oDel);
-    if (NJ != 1) {
-      constexpr int L = D / 8, R = 32 / L;  // lanes of a row, rows of a warp at a time
+    bool ok = true;
+    if (NJ > 1) {
+      constexpr int CH = D / 8;  // 16-byte chunks of a row
+      uint8_t* tO = smem + Lay::oK + 2 * Lay::kTile;
+      uint8_t* tL = smem + Lay::oV + Lay::kTile;
 #pragma unroll 4
-      for (int i = 0; i < 16 / R; ++i) {
-        const int r = warp * 16 + i * R + lane / L, qq = qt * 128 + r, c = lane % L * 8;
-        float sum = 0.f;
-        if (qq < a.N) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(O) + b * so.b +
-                                                               h * so.h + (int64_t)qq * so.n + c));
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(dO) + b * sdo.b +
-                                                               h * sdo.h + (int64_t)qq * sdo.n + c));
-          const uint4 v = Olow ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(Olow) +
-                                                                      ((int64_t)bh * a.N + qq) * D + c))
-                               : make_uint4(0, 0, 0, 0);
-          const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, wa[4] = {w.x, w.y, w.z, w.w}, va[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 x = unpack2<F16>(ua[e]), y = unpack2<F16>(wa[e]), z = unpack2<F16>(va[e]);
-            sum = fmaf(x.x + z.x, y.x, fmaf(x.y + z.y, y.y, sum));
-          }
+      for (int i = threadIdx.x; i < 128 * CH; i += kCompute) {
+        const int r = i / CH, c = i % CH, n = qt * 128 + r;
+        const int live = n < a.N ? 16 : 0;
+        const uint16_t* po = reinterpret_cast<const uint16_t*>(O) + b * so.b + h * so.h + (live ? (int64_t)n * so.n + c * 8 : 0);
+        const uint32_t at = r * (D * 2) + ((c ^ (r & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tO + at)), "l"(po), "r"(live) : "memory");
+        if (Olow) {
+          const uint16_t* pl = reinterpret_cast<const uint16_t*>(Olow) + (live ? ((int64_t)bh * a.N + n) * D + c * 8 : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tL + at)), "l"(pl), "r"(live)
+                       : "memory");
         }
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane % L == 0) sDel[r] = sum;
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      ok = __all_sync(0xffffffffu, mbar_wait(bQO, 0, abort_flag));
+      compute_sync_q();
+      float sum = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < CH / 2; ++i) {
+        const int c = g * (CH / 2) + i;
+        const int at = t * (D * 2) + ((c ^ (t & 7)) << 4);
+        const uint4 u = *reinterpret_cast<const uint4*>(tO + at);
+        const uint4 v = Olow ? *reinterpret_cast<const uint4*>(tL + at) : make_uint4(0, 0, 0, 0);
+        const uint4 w = *reinterpret_cast<const uint4*>(smem + Lay::oO + (c >> 3) * kRegion + t * 128 +
+                                                        (((c & 7) ^ (t & 7)) << 4));
+        const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, wa[4] = {w.x, w.y, w.z, w.w}, va[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = unpack2<F16>(ua[e]), y = unpack2<F16>(wa[e]), z = unpack2<F16>(va[e]);
+          sum = fmaf(x.x + z.x, y.x, fmaf(x.y + z.y, y.y, sum));
+        }
+      }
+      fence_proxy_async_smem();  // before the copies of the producer over what was read
+      mbar_arrive(bDel);
+      sDel[g * 128 + t] = sum;
+      compute_sync_q();
     }
-    compute_sync_q();
-    float del = NJ != 1 ? sDel[t] : 0.f;
+    float del = NJ > 1 ? sDel[t] + sDel[128 + t] : 0.f;
     const float lse_raw = q < a.N ? a.lse[(int64_t)bh * a.N + q] : -INFINITY;
     const float lse = lse_raw == -INFINITY ? INFINITY : lse_raw * kLog2e;  // no key: P = 2^-inf = 0
     const float scale_log2 = a.scale * kLog2e;
@@ -678,7 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (NJ != 1 && g == 0 && q < a.N) a.delta[(int64_t)bh * a.N + q] = del;
     uint64_t d2 = f2_pack(del, del);
     const Mod mod = MOD ? make_mod(a, h) : Mod{};
-    bool ok = true;
     for (int j = 0; j < NJ; ++j) {
       const int buf = j & 1;
       const int kb = (k0 + j) * 128;
