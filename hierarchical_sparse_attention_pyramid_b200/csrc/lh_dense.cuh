@@ -139,6 +139,25 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
   if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
+
+// Outputs of a tile leave a warp as whole lines: its 32 rows of CW bytes lie in
+// shared memory, 16-byte chunk c of row r at line_at<CW>(r, c) (8 neighbouring
+// rows meet different banks), and go to rows of `dst`, of which `rows` are.
+template <int CW>
+__device__ __forceinline__ int line_at(int r, int c) {
+  return r * CW + ((c ^ (r & (CW / 16 - 1))) << 4);
+}
+template <int CW>
+__device__ __forceinline__ void store_lines(const uint8_t* lines, uint16_t* dst, int64_t stride, int rows, int lane) {
+  constexpr int CH = CW / 16;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int r = i * (32 / CH) + lane / CH;
+    if (r < rows)
+      *reinterpret_cast<uint4*>(dst + r * stride + lane % CH * 8) =
+          *reinterpret_cast<const uint4*>(lines + line_at<CW>(r, lane % CH));
+  }
+}
 template <bool F16>
 __host__ __device__ constexpr uint32_t idesc16(int M, int N, bool a_mn, bool b_mn) {
   return F16 ? sm100::idesc_f16(M, N, a_mn, b_mn) : sm100::idesc_bf16(M, N, a_mn, b_mn);
@@ -210,7 +229,7 @@ cudaError_t launch_dense_fwd(const DenseArgs& a, int d, bool f16, const CUtensor
                              const CUtensorMap& v, void* o, const Strides& so, void* o_low, cudaStream_t st);
 cudaError_t launch_dense_bwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, const CUtensorMap& go, const void* o, const Strides& so,
-                             const void* o_low, const void* dout, const Strides& sdo, void* dq, const Strides& sdq, void* dk,
-                             const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st);
+                             const void* o_low, void* dq, const Strides& sdq, void* dk, const Strides& sdk, void* dv,
+                             const Strides& sdv, cudaStream_t st);
 
 }  // namespace lh

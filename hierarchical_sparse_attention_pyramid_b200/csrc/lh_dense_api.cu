@@ -194,8 +194,8 @@ lh_status lh_dense_bwd(const lh_dense_config* cfg, const void* q, const void* k,
       !make_head_map(&mo, dout, cfg->dtype, cfg->B, cfg->Hq, cfg->N, cfg->d, cfg->do_stride))
     return fail(LH_ERR_CUDA, kCall, "no tensor map for these strides");
   return done(launch_dense_bwd(a, cfg->d, cfg->dtype == LH_FP16, mq, mk, mv, mo, o, strides_of(cfg->o_stride), o_low,
-                               dout, strides_of(cfg->do_stride), dq, strides_of(cfg->dq_stride), dk,
-                               strides_of(cfg->dk_stride), dv, strides_of(cfg->dv_stride), (cudaStream_t)stream),
+                               dq, strides_of(cfg->dq_stride), dk, strides_of(cfg->dk_stride), dv,
+                               strides_of(cfg->dv_stride), (cudaStream_t)stream),
               kCall);
 }
 

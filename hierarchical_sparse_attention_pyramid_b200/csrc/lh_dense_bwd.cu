@@ -26,8 +26,8 @@
 // gradients themselves.  The score scale is left out of dS and applied to the
 // fp32 sums: with fp16 that keeps small dS out of the subnormal range.
 //
-// Bound by the tensor cores: 16K causal tokens, 8 heads of 128: 623 us for dQ's
-// three products (1.32 PFLOP/s) and 843 us for the other four (1.30), near the
+// Bound by the tensor cores: 16K causal tokens, 8 heads of 128: 590 us for dQ's
+// three products (1.40 PFLOP/s) and 840 us for the other four (1.31), near the
 // 1.37 that a long product of large matrices sustains under the power limit.
 #include <type_traits>
 
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dense_bwd_q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                        const __grid_constant__ DenseArgs a, const void* __restrict__ O, const Strides so,
-                       const void* __restrict__ Olow, const void* __restrict__ dO, const Strides sdo, void* __restrict__ dQ, const Strides sdq) {
+                       const void* __restrict__ Olow, void* __restrict__ dQ, const Strides sdq) {
   using Lay = QSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -829,34 +829,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(bPS);
     }
     if (NJ > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(bDone, 0, abort_flag));
-    if (ok) {
+    if (ok) {  // out through the first K stage, which no product or copy uses any more
       tc_fence_after();
-#pragma unroll 1
+      constexpr int CW = D;  // bytes of the warpgroup's half of a row
+      uint8_t* lines = smem + Lay::oK + warp * (32 * CW);
+      uint32_t rv[D / 64][32];
+      if (NJ > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) tmem_ld32(tl + tDQ + g * (D / 2) + c * 32, rv[c]);
+        tmem_ld_wait();
+      }
+#pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const int col = g * (D / 2) + c * 32;
-        uint32_t r[32];
-        if (NJ > 0) {
-          tmem_ld32(tl + tDQ + col, r);
-          tmem_ld_wait();
-        }
+        uint32_t (&r)[32] = rv[c];
         if (NJ == 0 || len == 0) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0u;
         }
-        if (q < a.N) {
-          uint4* dq4 = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dQ) + b * sdq.b + h * sdq.h +
-                                                (int64_t)q * sdq.n + col);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack2<F16>(__uint_as_float(r[8 * i + 2 * e]) * a.scale,
-                                __uint_as_float(r[8 * i + 2 * e + 1]) * a.scale);
-            dq4[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack2<F16>(__uint_as_float(r[8 * i + 2 * e]) * a.scale, __uint_as_float(r[8 * i + 2 * e + 1]) * a.scale);
+          *reinterpret_cast<uint4*>(lines + line_at<CW>(lane, c * 4 + i)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+      __syncwarp();
+      const int q0 = q - lane;
+      store_lines<CW>(lines, reinterpret_cast<uint16_t*>(dQ) + b * sdq.b + h * sdq.h + (int64_t)q0 * sdq.n + g * (D / 2),
+                      sdq.n, a.N - q0, lane);
     }
   }
   tc_fence_before();
@@ -870,9 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, bool F16, bool MOD>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& go,
-                   const DenseArgs& a, const void* o, const Strides& so, const void* o_low, const void* dout,
-                   const Strides& sdo, void* dq, const Strides& sdq, void* dk, const Strides& sdk, void* dv,
-                   const Strides& sdv, cudaStream_t st) {
+                   const DenseArgs& a, const void* o, const Strides& so, const void* o_low, void* dq,
+                   const Strides& sdq, void* dk, const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st) {
   const int64_t gq = (int64_t)a.n_tiles * a.B * a.Hq, gk = (int64_t)a.n_tiles * a.B * a.Hkv;
   if (gq > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   auto* fq = dense_bwd_q_kernel<D, F16, MOD>;
@@ -881,7 +882,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(fk, cudaFuncAttributeMaxDynamicSharedMemorySize, KvSmem<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  fq<<<dim3((unsigned)gq), kThreads, QSmem<D>::kAlloc, st>>>(q, k, v, go, a, o, so, o_low, dout, sdo, dq, sdq);
+  fq<<<dim3((unsigned)gq), kThreads, QSmem<D>::kAlloc, st>>>(q, k, v, go, a, o, so, o_low, dq, sdq);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Few key tiles leave SMs idle: then a cluster of 2, 4 or 8 CTAs shares the
@@ -909,12 +910,12 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
 
 cudaError_t launch_dense_bwd(const DenseArgs& a, int d, bool f16, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, const CUtensorMap& go, const void* o, const Strides& so,
-                             const void* o_low, const void* dout, const Strides& sdo, void* dq, const Strides& sdq,
-                             void* dk, const Strides& sdk, void* dv, const Strides& sdv, cudaStream_t st) {
+                             const void* o_low, void* dq, const Strides& sdq, void* dk, const Strides& sdk, void* dv,
+                             const Strides& sdv, cudaStream_t st) {
   const bool mod = a.softcap > 0.f || a.slopes;
   auto pick = [&](auto D, auto F, auto M) {
-    return launch<decltype(D)::value, decltype(F)::value, decltype(M)::value>(q, k, v, go, a, o, so, o_low, dout, sdo, dq,
-                                                                              sdq, dk, sdk, dv, sdv, st);
+    return launch<decltype(D)::value, decltype(F)::value, decltype(M)::value>(q, k, v, go, a, o, so, o_low, dq, sdq, dk,
+                                                                              sdk, dv, sdv, st);
   };
   using T = std::true_type;
   using N = std::false_type;
