@@ -22,7 +22,7 @@
 // enters its score.
 //
 // One sequence of 512K int8 tokens, 4 key heads of 128: 86 us (6.4 TB/s); 64
-// sequences of up to 8K e4m3 tokens: 41 us against 36 for a copy of the bytes.
+// sequences of up to 8K e4m3 tokens: 41 us against 35 for a copy of the bytes.
 //
 // A block of 4 warps takes its stretch of the work list (lh_cache_attn.cuh)
 // for 8, 16 or 32 query rows of a head; the warps' running maxima, sums and

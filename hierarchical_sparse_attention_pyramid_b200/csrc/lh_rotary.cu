@@ -9,7 +9,7 @@
 // token and not once per head.  The angle is reduced to a fraction of a turn
 // in 64 bits (in 32 a position of 10^6 leaves no digits of the fraction) and
 // only the fraction goes to the 32-bit sincospi.  128K tokens of 20 heads of 128
-// in bf16, there and back: 446 us, 6.1 TB/s (93% of a copy).
+// in bf16, there and back: 446 us, 6.0 TB/s (92% of a copy).
 #include <type_traits>
 
 #include "lh_common.cuh"
