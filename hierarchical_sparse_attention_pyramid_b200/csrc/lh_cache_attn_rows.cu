@@ -80,12 +80,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
   __shared__ int64_t scan[kWarps + 1];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::oBar);
   uint64_t* bQ = bars + 0;     // Q of a piece written (128 arrivals)
-  uint64_t* bFull = bars + 1;  // [2] K, V and scales of a unit written (256 arrivals)
-  uint64_t* bFree = bars + 3;  // [2] its products done
+  uint64_t* bFull = bars + 1;  // [2] K, V and scales of a unit written (128 arrivals)
+  uint64_t* bFree = bars + 3;  // [2] its products done: the stage is free, O holds its P V.  One barrier a stage, so
+                               // that a softmax warp that is a unit ahead of another cannot take the unit before
+                               // for its own: bS of unit i comes after the products of unit i - 2
   uint64_t* bS = bars + 5;     // [2] S of a unit in a TMEM buffer
   uint64_t* bP = bars + 7;     // [2] P of a unit in its TMEM buffer, O rescaled (128 arrivals; a warp may be at the
                                // next unit already when another arrives)
-  uint64_t* bO = bars + 9;     // P V of a unit done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::oBar + 192);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::oBar + 196);
   volatile int* flag = reinterpret_cast<volatile int*>(smem + Lay::oFlag);
@@ -105,7 +106,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
       mbar_init(&bS[i], 1);
       mbar_init(&bP[i], 128);
     }
-    mbar_init(bO, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -148,7 +148,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
           umma_bf16_tmem_a_w(tmem + 256, tmem + st * 128 + kk * 8,
                              mV + ((st * Lay::kTile + kk * 2048) >> 4), idPV, (key > piece.k0 || kk > 0) ? 1u : 0u);
         umma_commit_w(&bFree[st]);
-        umma_commit_w(bO);
       }
     }
   } else if (warp >= 4) {
@@ -253,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16), to = tl + 256;
     const bool cap = a.softcap > 0.f;
     const float pre = cap ? a.scale / a.softcap : a.scale * kLog2e, cap2 = a.softcap * kLog2e;
+    auto products_done = [&](int i) { return mbar_wait(&bFree[i & 1], (i >> 1) & 1, abort_flag); };
     while (ok && next_piece(a, kRows, stretch, seq, piece)) {
       const int n_rows = seq.T * G, r = piece.rt * kRows + t, ctx = seq.len - seq.T;
       const bool live = r < n_rows;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
           vf = __uint_as_float(0x7f000000u - __float_as_uint(v_ref)) * kPUp;
         }
         if (it > first && __any_sync(0xffffffffu, move || lift)) {  // O, once the previous P V has added to it
-          ok = __all_sync(0xffffffffu, mbar_wait(bO, (it - 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, products_done(it - 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
         tc_fence_before();
         mbar_arrive(&bP[st]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bO, (it - 1) & 1, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, products_done(it - 1));
       if (!ok) break;
       tc_fence_after();
       if (!idle) {

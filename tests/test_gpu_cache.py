@@ -231,6 +231,31 @@ def test_cache_attention_long_and_many():
         du.check("o", got, (value, bound))
 
 
+@pytest.mark.parametrize("kind,d", [("bf16", 64), ("int8", 128)])
+def test_rows_of_a_tile_at_different_pace(kind, d):
+    """Tiles of 128 rows whose first 32 rows keep one maximum while the others' grows with every 128 keys, so that the
+    first warp of a tile is ahead of the others (which rescale their outputs each time) when the keys end."""
+    heads, G, lens = 2, 128, (2048, 250, 384, 1, 129)
+    table, pages, slots = paging(lens, 64)
+    cache = lh.KVCache.empty(pages, heads, 64, d, kind)
+    n = sum(lens)
+    k, v = randn((n, heads, d), torch.float32, 1, 0.1), randn((n, heads, d), torch.float32, 2)
+    k[:, :, 0] = torch.cat([torch.arange(m) // 128 for m in lens]).cuda()[:, None].float()
+    lh.cache_write(cache, k, v, slots)
+    ks, vs = (t.double() for t in lh.cache_read(cache, table, starts_of(lens), n, dtype=torch.float32))
+    cut = [0] + torch.tensor(lens).cumsum(0).tolist()
+    ks, vs = ([t[a:b] for a, b in zip(cut, cut[1:])] for t in (ks, vs))
+    q = randn((len(lens), heads * G, d), torch.bfloat16, 5, 0.3)
+    q.view(len(lens), heads, G, d)[:, :, :32, 0] = 0
+    q.view(len(lens), heads, G, d)[:, :, 32:, 0] = 160.0  # the maximum moves by about 14 (20) with each unit of 128 keys
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = lh.cache_attention(cache, q, table, ln)
+    du.check("o", got, du.cache_attention64(q, ks, vs, list(range(len(lens) + 1)), lens))
+    for _ in range(50):
+        assert torch.equal(got, lh.cache_attention(cache, q, table, ln))
+    lh.check_dense_error()
+
+
 def test_cache_attention_values_of_any_size():
     """Value rows of very different size in one 8-bit cache, and tiny ones: none underflows on the way."""
     lens = (70,)
