@@ -116,6 +116,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
   int it = 0;  // units so far, over all pieces: ring stage and S buffer it & 1
   bool ok = true;
+  // A sequence of length 0 that has query tokens is a piece without keys (always
+  // a whole one: its only unit past kBegin).  No role counts a unit for it; the
+  // softmax warps write its zeros.
+  auto next_with_keys = [&]() -> bool {
+    while (next_piece(a, kRows, stretch, seq, piece))
+      if (piece.k0 < piece.k1) return true;
+    return false;
+  };
 
   if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
@@ -135,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
       umma_commit_w(&bS[i & 1]);
       return true;
     };
-    for (int n = 0; ok && next_piece(a, kRows, stretch, seq, piece); ++n) {
+    for (int n = 0; ok && next_with_keys(); ++n) {
       ok = mbar_wait_warp(bQ, n & 1, abort_flag) && issue_s(it);
       for (int key = piece.k0; ok && key < piece.k1; key += kUnit, ++it) {
         if (key + kUnit < piece.k1) ok = issue_s(it + 1);
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
       }
       rows = look_up(key + kUnit);
     };
-    bool have = next_piece(a, kRows, stretch, seq, piece);
+    bool have = next_with_keys();
     int key = have ? piece.k0 : 0;
     if (have) rows = look_up(key);
     if (HELD8 && have) load(key, nullptr, nullptr);
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
       mbar_arrive(&bFull[st]);
       key += kUnit;
       if (key >= piece.k1) {
-        have = next_piece(a, kRows, stretch, seq, piece);
+        have = next_with_keys();
         key = piece.k0;
         if (have) rows = look_up(key);
       }
@@ -258,6 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
       const bool live = r < n_rows;
       const bool idle = piece.rt * kRows + warp * 32 >= n_rows;  // no row of the warp is one
       const int64_t out = live ? (int64_t)(seq.tok0 + r / G) * a.Hq + piece.hk * G + r % G : 0;
+      if (piece.k0 >= piece.k1) {
+        for (int i = 0; live && i < D / 8; ++i)
+          reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D)[i] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
       // the row of Q, with 8-bit keys times the power of two that brings its
       // largest value to [2^14, 2^15)
       float up = 1.f;

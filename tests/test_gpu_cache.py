@@ -256,6 +256,38 @@ def test_rows_of_a_tile_at_different_pace(kind, d):
     lh.check_dense_error()
 
 
+@pytest.mark.parametrize("kind,dtype,G,d,tree", [("e4m3", torch.bfloat16, 40, 64, 0), ("int8", torch.float16, 33, 128, 0),
+                                                 ("bf16", torch.bfloat16, 48, 64, 0), ("fp16", torch.float16, 33, 128, 0),
+                                                 ("e4m3", torch.bfloat16, 6, 64, 1), ("bf16", torch.bfloat16, 5, 128, 1),
+                                                 ("int8", torch.bfloat16, 4, 64, 0)])
+def test_empty_sequences_between_others(kind, dtype, G, d, tree):
+    """Query tokens of sequences of length 0 (unused places of a batch) get zeros and leave the other sequences alone:
+    empty ones first, last, alone and several in a row, in stretches of several sequences and heads a block."""
+    some = [0, 0, 130, 1, 0, 257, 0, 0, 0, 64, 300, 0, 129, 128, 0]
+    lens = tuple(some[i % len(some)] if i % 7 else 0 for i in range(210)) + (700, 0, 0, 0)
+    cache, table, ks, vs = filled(kind, lens, 4, d, 16)
+    T = [8] * len(lens) if tree else [1] * len(lens)
+    masks = None
+    if tree:
+        masks = random_tree(T, 3).cuda()
+        # a tree has its tokens in the cache: short sequences have as many as they have positions
+        T = [8 if n == 0 or n >= 8 else n for n in lens]
+        keep = torch.cat([torch.arange(8) < t for t in T])
+        masks = masks[keep.cuda()].contiguous()
+    n, Hq = sum(T), 4 * G
+    q = randn((n, Hq, d), dtype, 5, 1.5)
+    cut = [0] + torch.tensor(T).cumsum(0).tolist()
+    opt = dict(q_start=torch.tensor(cut, dtype=torch.int32, device="cuda"), max_tokens=max(T), tree_mask=masks)
+    got = lh.cache_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), **opt)
+    lh.check_dense_error()
+    for s, length in enumerate(lens):
+        if length == 0:
+            assert (got[cut[s]:cut[s + 1]] == 0).all(), s
+    value, bound = du.cache_attention64(q, ks, vs, cut, lens, None if masks is None else
+                                        [x & (1 << 64) - 1 for x in masks.tolist()])
+    du.check("o", got, (value, bound))
+
+
 def test_cache_attention_values_of_any_size():
     """Value rows of very different size in one 8-bit cache, and tiny ones: none underflows on the way."""
     lens = (70,)
