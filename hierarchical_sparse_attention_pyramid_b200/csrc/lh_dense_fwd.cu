@@ -255,11 +255,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
               mc[ch * 4 + (i >> 3)] =
-                  max3f(mc[ch * 4 + (i >> 3)], __uint_as_float(r[ch][i]), __uint_as_float(r[ch][i + 1]));
+                  max3f_nan(mc[ch * 4 + (i >> 3)], __uint_as_float(r[ch][i]), __uint_as_float(r[ch][i + 1]));
         }
       }
       if constexpr (MOD) tmem_st_wait();
-      const float mx = fmaxf(fmaxf(max3f(mc[0], mc[1], mc[2]), max3f(mc[3], mc[4], mc[5])), fmaxf(mc[6], mc[7]));
+      const float mx = max3f_nan(max3f_nan(mc[0], mc[1], mc[2]), max3f_nan(mc[3], mc[4], mc[5]),
+                                 max3f_nan(mc[6], mc[7], -INFINITY));
       // The reference moves only when the maximum exceeds it by more than 8
       // (P stays <= 2^8); O and l share it, so the result is exact either way.
       const float m_tile = mx * scale_log2;
@@ -335,8 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q.y <= q.x) zero_row(smem + Lay::oV + (i & 1) * Lay::kTile, t, 0, D / 64);
         fence_proxy_async_smem();
       }
-      // masked tiles, and rows whose scores are beyond 2^16 in size
-      if (!MOD && (!full || __any_sync(0xffffffffu, fabsf(m_ref) > 65536.f))) p_pass(std::true_type{});
+      // masked tiles, and rows whose scores are beyond 2^16 in size, have a NaN or
+      // are all -inf (the polynomial exponentials would make numbers of those)
+      if (!MOD && (!full || __any_sync(0xffffffffu, !(fabsf(m_new) <= 65536.f) || mx != mx))) p_pass(std::true_type{});
       else p_pass(std::false_type{});
       float rsa, rsb;
       f2_unpack(f2_add(rs2[0], rs2[1]), rsa, rsb);

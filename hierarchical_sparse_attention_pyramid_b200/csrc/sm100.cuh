@@ -266,14 +266,14 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// 2^x of a pair on the FMA pipes (x <= 127; below -126 it returns 2^-126):
-// x = n + f with n the nearest integer, 2^f by the polynomial of degree 4
+// 2^x of a pair on the FMA pipes, for numbers x <= 127 (a NaN is lost; from
+// -127 down it returns 2^-149, which the 16-bit types round to 0): x = n + f with n the nearest integer, 2^f by the polynomial of degree 4
 // that interpolates it at Chebyshev points of [-1/2, 1/2] (relative error
 // 4e-6), n added to the exponent bits
 __device__ __forceinline__ void poly_exp2(uint64_t x, float& a, float& b) {
   float lo, hi;
   f2_unpack(x, lo, hi);
-  x = f2_pack(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
+  x = f2_pack(fmaxf(lo, -127.f), fmaxf(hi, -127.f));
   const uint64_t magic = f2_pack(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low bits are n
   const uint64_t n = f2_add(x, magic);
   const uint64_t f = f2_sub(x, f2_sub(n, magic));
@@ -286,6 +286,12 @@ __device__ __forceinline__ void poly_exp2(uint64_t x, float& a, float& b) {
   f2_unpack(p, a, b);
   a = __uint_as_float(__float_as_uint(na) * 8388608u + __float_as_uint(a));
   b = __uint_as_float(__float_as_uint(nb) * 8388608u + __float_as_uint(b));
+}
+// the largest of three, NaN if one is NaN
+__device__ __forceinline__ float max3f_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;

@@ -502,7 +502,8 @@ typedef struct {
  * pointers 16-byte aligned.
  * Out: o; lse [B][Hq][N] fp32, the natural log of the row's sum of
  * exponentials; o_low [B][Hq][N][d] in the inputs' type, contiguous, or NULL:
- * what rounding to o took off (for lh_dense_bwd).  A query without keys has O = 0 and LSE = -inf.
+ * what rounding to o took off (for lh_dense_bwd).  A query without keys, or whose scores are all -inf, has O = 0 and
+ * LSE = -inf; one that sees a score of NaN or +inf is NaN.
  * Probabilities enter P V rounded to the inputs' type; sums are fp32.  Values
  * in padding and past N are not used; those of another document of the batch
  * row must be finite. */

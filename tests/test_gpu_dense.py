@@ -242,6 +242,63 @@ def test_scores_of_the_lowest_values():
     assert torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("heads", [128, 16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_scores_that_are_not_finite(value, heads, cap):
+    """A NaN or infinite score at every column of the unmasked and masked key tiles (head h: key 128 / heads * h), in
+    calls of one and of two query tiles a CTA: every query that sees a NaN or +inf is NaN, one that sees -inf gives the
+    key no weight whatever its value is, the others know nothing of it."""
+    N, d = 384, 64
+    q, k, v = (randn((1, heads, N, d), torch.bfloat16, s) for s in (1, 2, 3))
+    q[..., 0] = 1.0
+    for step in range(128 // heads):
+        for causal in (True, False):
+            j = torch.arange(heads, device="cuda") * (128 // heads) + step
+            bad, big = k.clone(), v.clone()
+            bad[0, torch.arange(heads), j, 0] = value
+            if value < 0 and not cap:
+                big[0, torch.arange(heads), j] = 3e38
+            o, (lse, _) = lh.dense_forward(q, bad, big, causal=causal, softcap=cap)
+            i = torch.arange(N, device="cuda")
+            sees = (i >= j[:, None]) if causal else torch.ones(heads, N, dtype=torch.bool, device="cuda")
+            x = (q.double() @ k.double().transpose(-1, -2)) / math.sqrt(d)
+            if cap:
+                x = cap * torch.tanh(x / cap)
+            hide = torch.zeros(heads, N, N, dtype=torch.bool, device="cuda")
+            if causal:
+                hide |= i > i[:, None]
+            at = torch.zeros_like(hide)
+            at[torch.arange(heads), :, j] = True
+            if cap and not math.isnan(value):  # a score of +-cap
+                x = torch.where(at, math.copysign(cap, value), x)
+                lost = torch.zeros_like(sees)
+            elif value < 0:
+                hide = hide | at
+                lost = torch.zeros_like(sees)
+            else:
+                lost = sees
+            assert o[0][lost].isnan().all() and lse[0][lost].isnan().all()
+            x = x[0].masked_fill(hide, -math.inf)
+            p = torch.softmax(x, -1)
+            none = hide.all(-1)
+            p = p.masked_fill(none[..., None], 0.0)
+            u = du.half_step(torch.bfloat16)
+            want, size = p @ v[0].double(), p @ v[0].double().abs()
+            keep = ~lost
+            du.check("o", o[0][keep], (want[keep], (u * want.abs() + (u + du.F) * size + 1e-30)[keep]))
+            lse64 = torch.logsumexp(x, -1)
+            du.check("lse", lse[0][keep], (lse64[keep], (2.0 ** -18 * (1 + lse64.abs().clamp_max(1e6)))[keep]))
+            assert (o[0][none] == 0).all()
+    # nothing but -inf: no weight anywhere, as for a query without keys
+    if value < 0 and not cap:
+        bad = k.clone()
+        bad[..., 0] = value
+        for causal in (True, False):
+            o, (lse, _) = lh.dense_forward(q, bad, v, causal=causal)
+            assert (o == 0).all() and (lse == -math.inf).all()
+
+
 def test_gradient_against_differences():
     """The gradient of a weighted sum of outputs, against central differences of the fp64 form."""
     case = (1, 2, 1, 20, 64, "fp16", 1, 1, True, 8.0, 1, 0)
