@@ -372,11 +372,12 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int r = min(r0 + nb * 8 + 2 * t + x, n_rows - 1);
-            const float slope2 = __ldg(a.slopes + hk * G + r % G) * kLog2e, at = (float)(ctx + r / G);
+            // the distance as a whole number first: positions past 2^24 are none in fp32
+            const float slope2 = __ldg(a.slopes + hk * G + r % G) * kLog2e, d0 = (float)(ctx + r / G - key - g);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
               float& y = sc[nb][j / 2][2 * (j & 1) + x];
-              y = fmaf(-slope2, fabsf(at - (float)(key + 8 * j + g)), y);
+              y = fmaf(-slope2, fabsf(d0 - (float)(8 * j)), y);
             }
           }
         }

@@ -288,6 +288,27 @@ def test_empty_sequences_between_others(kind, dtype, G, d, tree):
     du.check("o", got, (value, bound))
 
 
+@pytest.mark.parametrize("G", [1, 12, 20, 40])
+def test_distances_of_positions_past_2_to_the_24(G):
+    """A distance bias over 33 million positions (all columns of the table but the last on one page): the weights of the
+    newest keys go by their exact distances, which positions in fp32 would not give."""
+    d, page, width = 64, 4096, 8194
+    n = (width - 2) * page + page + 37  # 2^25 + 4133
+    cache = lh.KVCache.empty(3, 1, page, d, "int8")
+    k, v = randn((3 * page, 1, d), torch.float32, 1), randn((3 * page, 1, d), torch.float32, 2)
+    lh.cache_write(cache, k, v, torch.arange(3 * page, device="cuda"))
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    table[0, -2:] = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    q = randn((1, G, d), torch.bfloat16, 5)
+    slopes = torch.tensor([1.0 + 0.125 * (h % 8) for h in range(G)], device="cuda")
+    got = lh.cache_attention(cache, q, table, torch.tensor([n], dtype=torch.int32, device="cuda"), slopes=slopes)
+    lh.check_dense_error()
+    near = page + 37  # the keys of the last two pages; the others' weights are below e^-4000
+    ks, vs = (t.double() for t in lh.cache_read(cache, table[:, -2:].contiguous(), starts_of((near,)), near,
+                                                dtype=torch.float32))
+    du.check("o", got, du.cache_attention64(q, [ks], [vs], [0, 1], (near,), slopes=slopes))
+
+
 def test_cache_attention_values_of_any_size():
     """Value rows of very different size in one 8-bit cache, and tiny ones: none underflows on the way."""
     lens = (70,)
