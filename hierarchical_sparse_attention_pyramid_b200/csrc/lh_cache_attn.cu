@@ -363,10 +363,26 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
 #pragma unroll
           for (int x = 0; x < 2; ++x) sc[nb][j / 2][2 * (j & 1) + x] *= HELD8 ? kf[j] * qf[nb][x] : qf[nb][x];
         if (cap) {
+          float top = 0.f;
 #pragma unroll
           for (int k2 = 0; k2 < NT / 2; ++k2)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nb][k2][e] = cap2 * tanh_abs(sc[nb][k2][e]);
+            for (int e = 0; e < 4; e += 2) top = sm100::max3f(top, fabsf(sc[nb][k2][e]), fabsf(sc[nb][k2][e + 1]));
+          auto each = [&](auto near) {
+#pragma unroll
+            for (int k2 = 0; k2 < NT / 2; ++k2)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                float& x = sc[nb][k2][e];
+                float& y = sc[nb][k2][e + 1];
+                if constexpr (decltype(near)::value) tanh_near(x, y);
+                else tanh_any(x, y);
+                x *= cap2;
+                y *= cap2;
+              }
+          };
+          if (__all_sync(0xffffffffu, top <= 1.f)) each(std::true_type{});  // all below the cap
+          else each(std::false_type{});
         }
         if (bias) {
 #pragma unroll

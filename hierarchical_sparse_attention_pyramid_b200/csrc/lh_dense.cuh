@@ -16,6 +16,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "lh_common.cuh"
 #include "sm100.cuh"
 
@@ -163,44 +165,61 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, bool a_mn, bool b_m
   return F16 ? sm100::idesc_f16(M, N, a_mn, b_mn) : sm100::idesc_bf16(M, N, a_mn, b_mn);
 }
 
-// tanh from one exponential and one reciprocal: its absolute error (~1e-7) is
-// what matters, since the capped score is softcap * tanh
-__device__ __forceinline__ float tanh_abs(float y) {
+// tanh, to a relative 1.8e-7: the capped score is softcap * tanh, and a score
+// far below the cap keeps its own digits.  For |y| <= 1 the odd polynomial of
+// degree 13 that interpolates tanh(y) / y at Chebyshev points of y^2 in
+// [0, 1]; beyond, from one exponential and one reciprocal (absolute error 1e-7).
+// The polynomial needs neither, whose unit the softmax's own exponentials fill.
+__device__ __forceinline__ void tanh_near(float& a, float& b) {
+  using namespace sm100;
+  constexpr float c[7] = {0.99999994f, -0.33332857f, 0.13325398f, -0.053465176f, 0.02030552f, -0.00621707f,
+                          0.0010455536f};
+  const uint64_t y = f2_pack(a, b), u = f2_mul(y, y);
+  uint64_t p = f2_pack(c[6], c[6]);
+#pragma unroll
+  for (int k = 5; k >= 0; --k) p = f2_fma(p, u, f2_pack(c[k], c[k]));
+  f2_unpack(f2_mul(y, p), a, b);
+}
+__device__ __forceinline__ float tanh_far(float y) {
   float r;
   const float e = sm100::fast_exp2(y * (2.f * kLog2e));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
   return fmaf(-2.f, r, 1.f);
 }
+__device__ __forceinline__ void tanh_any(float& a, float& b) {
+  float na = a, nb = b;
+  tanh_near(na, nb);
+  a = fabsf(a) <= 1.f ? na : tanh_far(a);
+  b = fabsf(b) <= 1.f ? nb : tanh_far(b);
+}
+__device__ __forceinline__ float tanh_any(float y) {
+  float a = y, b = y;
+  tanh_any(a, b);
+  return a;
+}
 
-// tanh of 32 scores times `pre`, in place.  Where a warp's are all at most 1
-// in size (scores up to the cap), by the odd polynomial of degree 13 that
-// interpolates tanh(y) / y at Chebyshev points of y^2 in [0, 1]: its error in
-// fp32 arithmetic is 1.3e-7, as large as tanh_abs's, and it needs no
-// exponential or reciprocal, whose unit the softmax's own exponentials fill.
-__device__ __forceinline__ void cap_scores(uint32_t (&r)[32], float pre) {
-  using namespace sm100;
+// tanh of N scores times `pre`, in place; one vote of the warp settles whether
+// all of them are below the cap
+template <int N>
+__device__ __forceinline__ void cap_scores(uint32_t (&r)[N], float pre) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) top = max3f(top, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
-  if (__all_sync(0xffffffffu, top * pre <= 1.f)) {
-    constexpr float c[7] = {0.99999994f, -0.33332857f, 0.13325398f, -0.053465176f, 0.02030552f, -0.00621707f,
-                            0.0010455536f};
+  for (int i = 0; i < N; i += 2)
+    top = sm100::max3f(top, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+  auto each = [&](auto near) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const uint64_t y = f2_mul(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_pack(pre, pre));
-      const uint64_t u = f2_mul(y, y);
-      uint64_t p = f2_pack(c[6], c[6]);
-#pragma unroll
-      for (int k = 5; k >= 0; --k) p = f2_fma(p, u, f2_pack(c[k], c[k]));
+    for (int i = 0; i < N; i += 2) {
       float a, b;
-      f2_unpack(f2_mul(y, p), a, b);
+      sm100::f2_unpack(sm100::f2_mul(sm100::f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                     sm100::f2_pack(pre, pre)), a, b);
+      if constexpr (decltype(near)::value) tanh_near(a, b);
+      else tanh_any(a, b);
       r[i] = __float_as_uint(a);
       r[i + 1] = __float_as_uint(b);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(tanh_abs(__uint_as_float(r[i]) * pre));
-  }
+  };
+  if (__all_sync(0xffffffffu, top * pre <= 1.f)) each(std::true_type{});
+  else each(std::false_type{});
 }
 
 // Capped and biased scores: a score s becomes t = tanh(s pre) (capped, by

@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) {
               float x = __uint_as_float(sv[e]) * (MOD ? mod.mul : scale_log2);
               if constexpr (MOD) {
-                if (mod.cap) x = tanh_abs(__uint_as_float(sv[e]) * mod.pre) * mod.mul;
+                if (mod.cap) x = tanh_any(__uint_as_float(sv[e]) * mod.pre) * mod.mul;
                 if (mod.bias) x = fmaf(-mod.slope2, fabsf((float)(q - kb - g * 64 - ch * 16 - e)), x);
               }
               if ((unsigned)(ch * 16 + e - lo) < len) sum = fmaf(fast_exp2(x - lse), __uint_as_float(dv[e]), sum);

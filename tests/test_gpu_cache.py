@@ -309,6 +309,16 @@ def test_distances_of_positions_past_2_to_the_24(G):
     du.check("o", got, du.cache_attention64(q, [ks], [vs], [0, 1], (near,), slopes=slopes))
 
 
+@pytest.mark.parametrize("kind", ["fp16", "int8"])
+@pytest.mark.parametrize("G", [2, 12, 20, 40])
+def test_scores_far_below_a_large_cap(kind, G):
+    lens = (300, 40)
+    cache, table, ks, vs = filled(kind, lens, 1, 64, 16)
+    q = randn((2, G, 64), torch.float16, 5, 1.5)
+    got = lh.cache_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), softcap=2.0 ** 20)
+    du.check("o", got, du.cache_attention64(q, ks, vs, [0, 1, 2], lens, softcap=2.0 ** 20))
+
+
 def test_cache_attention_values_of_any_size():
     """Value rows of very different size in one 8-bit cache, and tiny ones: none underflows on the way."""
     lens = (70,)

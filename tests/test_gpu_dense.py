@@ -299,6 +299,24 @@ def test_scores_that_are_not_finite(value, heads, cap):
             assert (o == 0).all() and (lse == -math.inf).all()
 
 
+@pytest.mark.parametrize("N", [100, 300])
+def test_scores_far_below_a_large_cap(N):
+    """A cap of 2^16 over scores of ordinary size, beside rows whose scores reach it: the small ones keep their own
+    digits, not those of the cap."""
+    q, k, v, do = (randn((1, 2, N, 64), torch.float16, s, x) for s, x in ((1, 0.4), (2, 4.0), (3, 1.0), (4, 1.0)))
+    far = torch.zeros(N, dtype=torch.bool, device="cuda")
+    far[5::32] = True  # some in every warp
+    q[:, :, far] *= 32768.0
+    do[:, :, far] = 0  # no gradient passes through them
+    cap = 65536.0
+    o, saved = lh.dense_forward(q, k, v, softcap=cap)
+    grads = lh.dense_backward(do, q, k, v, o, saved, softcap=cap)
+    ref = du.attention64(q, k, v, do, du.seen_matrix(1, N, device="cuda"), 1 / 8.0, cap)
+    for n, got in zip(("o", "lse", "dq", "dk", "dv"), (o, saved.lse, *grads)):
+        keep = torch.ones_like(far) if n in ("dk", "dv") else ~far
+        du.check(n, got[:, :, keep], tuple(t[:, :, keep] for t in ref[n]))
+
+
 def test_gradient_against_differences():
     """The gradient of a weighted sum of outputs, against central differences of the fp64 form."""
     case = (1, 2, 1, 20, 64, "fp16", 1, 1, True, 8.0, 1, 0)
