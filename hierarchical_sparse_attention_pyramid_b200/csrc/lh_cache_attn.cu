@@ -271,8 +271,7 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
     float m[NB][2], l[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
-    float v_ref = 7.888609052210118e-31f;  // (2^-100) 8 bits: power of two at or above the value scales so far, which
-                                           // acc is relative to
+    float v_ref = kLeastScale;  // 8 bits: power of two at or above the value scales so far, which acc is relative to
     const uint32_t k_at = swz(g, t), v_at0 = swz(2 * t, g * VB >> 4) + (g * VB & 15),
                    v_at1 = swz(2 * t + 1, g * VB >> 4) + (g * VB & 15);
 
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, NB <= 2 ? 3 : 2)
         }
         if (__any_sync(0xffffffffu, v_new > v_ref)) {
           const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(v_new));
-          const float up = __uint_as_float(max(27u, min(227u, (top + 0x7fffffu) >> 23)) << 23);
+          const float up = scale_above(top);
           const float f = v_ref / up;
           v_ref = up;
 #pragma unroll

@@ -146,6 +146,14 @@ __device__ __forceinline__ uint32_t key_rows(const CacheAttnArgs& a, const int32
   return 0xffffffffu;
 }
 
+// The power of two that the values' scales are taken relative to: at or above
+// the largest one (bits of a scale above kLeastScale), whose reciprocal, raised
+// by the 2^6 of the probabilities, is finite.
+constexpr float kLeastScale = 3.7615819226313200e-37f;  // 2^-121
+__device__ __forceinline__ float scale_above(unsigned bits) {
+  return __uint_as_float(min(253u, (bits + 0x7fffffu) >> 23) << 23);
+}
+
 // two e4m3 bytes (the low half of y) as fp16
 __device__ __forceinline__ uint32_t e4m3_half2(uint32_t y) {
   uint32_t r;

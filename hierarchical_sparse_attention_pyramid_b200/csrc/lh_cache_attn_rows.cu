@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
       const int limit = live ? (a.tree ? ctx : ctx + tk + 1) : 0;  // keys below are seen
       const uint64_t bits = a.tree && live ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree) + seq.tok0 + tk) : 0;
       float m_run = -INFINITY, l_run = 0.f;
-      float v_ref = 7.888609052210118e-31f;  // (2^-100) 8 bits: power of two at or above the value scales so far
+      float v_ref = kLeastScale;  // 8 bits: power of two at or above the value scales so far
       const int first = it;
       for (int key = piece.k0; key < piece.k1; key += kUnit, ++it) {
         const int st = it & 1;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_rows_kernel(const __gr
               __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(0.f, fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)))));
           lift = __uint_as_float(top) > v_ref;
           if (lift) {
-            const float up_v = __uint_as_float(max(27u, min(227u, (top + 0x7fffffu) >> 23)) << 23);
+            const float up_v = scale_above(top);
             alpha *= v_ref / up_v;
             v_ref = up_v;
           }

@@ -319,6 +319,22 @@ def test_scores_far_below_a_large_cap(kind, G):
     du.check("o", got, du.cache_attention64(q, ks, vs, [0, 1, 2], lens, softcap=2.0 ** 20))
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("G", [4, 17, 40])
+def test_values_near_the_ends_of_fp32(kind, G):
+    """Value rows of 1e35 and of 1e-34, sizes that an 8-bit cache can hold in steps of its type."""
+    lens = (20, 5)
+    for size in (1e35, 1e-34):
+        table, pages, slots = paging(lens, 16)
+        cache = lh.KVCache.empty(pages, 1, 16, 64, kind)
+        k, v = randn((25, 1, 64), torch.float32, 1), randn((25, 1, 64), torch.float32, 2) * size
+        lh.cache_write(cache, k, v, slots)
+        ks, vs = (t.double() for t in lh.cache_read(cache, table, starts_of(lens), 25, dtype=torch.float32))
+        q = randn((2, G, 64), torch.bfloat16, 5)
+        got = lh.cache_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        du.check("o", got, du.cache_attention64(q, [ks[:20], ks[20:]], [vs[:20], vs[20:]], [0, 1, 2], lens))
+
+
 def test_cache_attention_values_of_any_size():
     """Value rows of very different size in one 8-bit cache, and tiny ones: none underflows on the way."""
     lens = (70,)
