@@ -13,8 +13,8 @@ import torch
 
 from . import _lib
 from ._lib import LhCache, LhCacheAttnConfig
-from .dense import (_NAMES, _are_tensors, _call, _contiguous_like, _err, _flat, _is_tensor, _keep, _not_tensors, _plans, _ptr, _sig,
-                    _tensor)
+from .dense import (_NAMES, _are_tensors, _call, _contiguous_like, _err, _flat, _is_tensor, _keep, _not_tensors,
+                    _plans, _ptr, _sig, _tensor, _writable, _written)
 
 _KINDS = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float8_e4m3fn: "e4m3", torch.int8: "int8"}
 
@@ -37,7 +37,8 @@ class KVCache:
         c = LhCache(pages, page, heads, d, _lib.CACHE_KINDS[kind], k.data_ptr(), v.data_ptr(), _ptr(k_scale),
                     _ptr(v_scale))
         self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, sig=sig, pages=pages, heads=heads, page=page,
-                             d=d, kind=kind, device=k.device, c=c, ref=ctypes.byref(c))
+                             d=d, kind=kind, device=k.device, c=c, ref=ctypes.byref(c),
+                             tensors=tuple(t for t in (k, v, k_scale, v_scale) if t is not None))
 
     @staticmethod
     def _check(k, v, k_scale, v_scale):
@@ -92,10 +93,13 @@ def cache_write(cache: KVCache, k, v, slots) -> None:
         i2 = ctypes.c_int64 * 2
         plan = _keep(key, (k.shape[0], _lib.DENSE_DTYPES[_NAMES[k.dtype]], i2(*k.stride()[:2]), i2(*v.stride()[:2])))
     n, dtype, k_stride, v_stride = plan
+    for name, t in (("cache.k", cache.k), ("cache.v", cache.v)):
+        _writable(name, t)
     if n:
         index = cache.device.index
         _call("lh_cache_write", index, cache.ref, n, dtype, k.data_ptr(), v.data_ptr(), k_stride, v_stride,
               slots.data_ptr(), _err(index))
+        _written(cache.tensors)
 
 
 def cache_read(cache: KVCache, page_table, starts, total: int, dtype=torch.bfloat16, out=None):
@@ -126,6 +130,8 @@ def cache_read(cache: KVCache, page_table, starts, total: int, dtype=torch.bfloa
     else:
         for name, t in zip(("out[0]", "out[1]"), out):
             _flat(name, t, cache.device, dtype, shape)
+            _writable(name, t)
+        _written(out)
     if total:
         index = cache.device.index
         _call("lh_cache_read", index, cache.ref, seqs, width, page_table.data_ptr(), starts.data_ptr(), total, code,
@@ -158,6 +164,8 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
         out = _contiguous_like(q)
     else:
         _flat("out", out, q.device, q.dtype, q.shape)
+        _writable("out", out)
+        _written(out)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     index = cache.device.index
     _call("lh_cache_attn", index, cache.ref, cfg, q.data_ptr(), page_table.data_ptr(), lens.data_ptr(), _ptr(q_start),

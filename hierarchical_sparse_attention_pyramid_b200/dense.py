@@ -8,7 +8,10 @@ Tensors are [B, H, N, d] with any batch, head and token strides that the
 kernels can address (channels contiguous; the attention: multiples of 8
 elements), so views of token-major projections need no copy.  The `*_forward`
 and `*_backward` calls and `rotary` refuse other tensors; `dense_attention` and
-`apply_rotary`, the autograd forms, copy them first.
+`apply_rotary`, the autograd forms, copy them first.  The others record no
+gradient: their results are detached, tensors that they are given to write
+must not require one while gradients are recorded, and count as modified in
+place.
 """
 
 from __future__ import annotations
@@ -77,6 +80,15 @@ def _call(name: str, index: int, *args) -> None:
     else:
         with torch.cuda.device(index):
             _lib.call(name, *args, stream)
+
+
+def _writable(name: str, t) -> None:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, and none is recorded for what is written into it")
+
+
+# what a call wrote through pointers counts as modified in place: a graph that saved it says so
+_written = torch.autograd.graph.increment_version
 
 
 def _ptr(t):
@@ -196,12 +208,17 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
         raise
     if len(outs) < len(ts):
         raise ValueError(f"out: {len(outs)} tensors, expected {len(ts)}")
+    if out is not None:
+        for i, o in enumerate(outs):
+            _writable(f"out[{i}]", o)
     cfg = _plans.get(key)
     if cfg is None:
         cfg = _keep(key, _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs))
     if q.numel() or (k is not None and k.numel()):
         _call("lh_rotary", q.device.index, cfg, q.data_ptr(), _ptr(k), frequencies.data_ptr(), _ptr(positions),
               outs[0].data_ptr(), outs[1].data_ptr() if k is not None else None)
+        if out is not None:
+            _written(outs)
     return outs[0], (outs[1] if k is not None else None)
 
 

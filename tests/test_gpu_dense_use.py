@@ -26,6 +26,47 @@ def test_inputs_changed_before_the_backward_are_refused():
             y.sum().backward()
 
 
+def test_written_tensors_count_as_modified():
+    """What the calls that record no gradient write is news to graphs that saved it, and they write no tensor that a
+    gradient is recorded for."""
+    f, _ = lh.rotary_frequencies(64)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    ln = torch.full((1,), 8, dtype=torch.int32, device="cuda")
+    slots = torch.arange(8, device="cuda")
+    cache = lh.KVCache.empty(1, 2, 8, 64, "bf16")
+    x = randn((8, 2, 64), torch.bfloat16, 1)
+    lh.cache_write(cache, x, x, slots)
+    q = randn((1, 2, 64), torch.bfloat16, 2)
+    starts = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    calls = [
+        ((1, 2, 5, 64), lambda t: lh.rotary(t, None, f, out=(t,))),
+        ((1, 2, 5, 64), lambda t: lh.rotary(t.clone(), t, f, out=(torch.empty_like(t), t))),
+        ((1, 2, 8, 64), lambda t: lh.cache_write(lh.KVCache(t, torch.zeros_like(t)), x, x, slots)),
+        ((1, 2, 8, 64), lambda t: lh.cache_write(lh.KVCache(torch.zeros_like(t), t), x, x, slots)),
+        ((8, 2, 64), lambda t: lh.cache_read(cache, table, starts, 8, out=(t, torch.empty_like(t)))),
+        ((8, 2, 64), lambda t: lh.cache_read(cache, table, starts, 8, out=(torch.empty_like(t), t))),
+        ((1, 2, 64), lambda t: lh.cache_attention(cache, q, table, ln, out=t)),
+    ]
+    for shape, call in calls:
+        leaf = randn(shape, torch.bfloat16, 3).requires_grad_()
+        t = leaf * 1
+        loss = (t * t).sum()
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call(t)
+        with torch.no_grad():
+            call(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        with torch.inference_mode():
+            call(torch.zeros(shape, dtype=torch.bfloat16, device="cuda"))
+    kept = lh.KVCache.empty(1, 2, 8, 64, "int8")
+    leaf = torch.ones(1, 2, 8, device="cuda", requires_grad=True)
+    loss = (leaf * kept.v_scale).sum()
+    lh.cache_write(kept, x, x, slots)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
 def test_second_derivatives_are_refused():
     x = [randn((1, 2, 40, 64), torch.bfloat16, s).requires_grad_() for s in (1, 2, 3)]
     for y in (lh.dense_attention(*x), lh.apply_rotary(x[0], None, lh.Rotary.make(64))):
