@@ -195,7 +195,8 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
 
     The first 2 * len(frequencies) channels of each head are turned: pairs (i, i + rot/2) with layout "half",
     (2i, 2i + 1) with "interleaved".  positions: int32 [B, N], or None for 0 .. N-1.  inverse turns back: the
-    gradient of a call is the inverse call on the output's gradient.  out: (q', k') to write, which may be (q, k)."""
+    gradient of a call is the inverse call on the output's gradient.  out: (q', k') to write, which may be (q, k) and
+    overlap them and each other in no other way."""
     ts = (q,) if k is None else (q, k)
     amplitude, inverse = float(amplitude), bool(inverse)
     try:
@@ -211,6 +212,9 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
     if out is not None:
         for i, o in enumerate(outs):
             _writable(f"out[{i}]", o)
+            for j, t in enumerate(ts + tuple(outs[:i])):  # the calls' own check: what begins at one place
+                if o.data_ptr() == t.data_ptr() and o.numel() and (i != j or o.stride() != t.stride()):
+                    raise ValueError(f"out[{i}]: overlaps another tensor of the call")
     cfg = _plans.get(key)
     if cfg is None:
         cfg = _keep(key, _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs))

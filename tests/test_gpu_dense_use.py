@@ -26,6 +26,23 @@ def test_inputs_changed_before_the_backward_are_refused():
             y.sum().backward()
 
 
+def test_rotary_refuses_outputs_over_other_tensors():
+    q, k = randn((1, 2, 6, 64), torch.bfloat16, 1), randn((1, 2, 6, 64), torch.bfloat16, 2)
+    f, _ = lh.rotary_frequencies(64)
+    want = lh.rotary(q, k, f)
+    o = torch.empty_like(q)
+    for out in ((k, q), (o, q), (k, o), (o, o), (q, q), (q.view(1, 6, 2, 64).transpose(1, 2), k)):
+        with pytest.raises(ValueError, match="overlaps"):
+            lh.rotary(q, k, f, out=out)
+    with pytest.raises(ValueError, match="overlaps"):
+        lh.rotary(q, None, f, out=(q.view(1, 6, 2, 64).transpose(1, 2),))
+    lh.rotary(q, k, f, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    # the same tensor for both, turned into two others
+    a, b = lh.rotary(q, q, f)
+    assert torch.equal(a, b)
+
+
 def test_written_tensors_count_as_modified():
     """What the calls that record no gradient write is news to graphs that saved it, and they write no tensor that a
     gradient is recorded for."""
