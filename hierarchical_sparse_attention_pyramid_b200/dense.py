@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -29,6 +30,7 @@ from ._lib import LhDenseConfig, LhRotaryConfig
 
 _NAMES = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
 _err_words: dict = {}
+_err_lock = threading.Lock()
 
 # Host plans of the calls (checked configurations), by the tensors' shapes,
 # strides, types and devices and the call's options: a program calls each
@@ -51,21 +53,26 @@ def _keep(key, plan):
 
 def _err(index: int):
     """Address of a device's error word: the calls below report into it (lh_check_error
-    clears it), see check_dense_error."""
+    clears it), see check_dense_error.  One a device for good: kernels in flight hold its address."""
     t = _err_words.get(index)
     if t is None:
-        if torch.cuda.is_current_stream_capturing():
-            return None  # the first call on a device is a captured one: not reported
-        with torch.cuda.device(index):
-            t = torch.zeros(_lib.ERR_WORD_BYTES, dtype=torch.uint8, device="cuda")
-            torch.cuda.current_stream().synchronize()
-        t = _err_words[index] = (t.data_ptr(), t)
+        with _err_lock, torch.cuda.device(index):
+            t = _err_words.get(index)
+            if t is None:
+                if torch.cuda.is_current_stream_capturing():
+                    return None  # the first call on a device is a captured one: not reported
+                t = torch.zeros(_lib.ERR_WORD_BYTES, dtype=torch.uint8, device="cuda")
+                torch.cuda.current_stream().synchronize()
+                t = _err_words[index] = (t.data_ptr(), t)
     return t[0]
 
 
 def check_dense_error(device=None) -> None:
     """Synchronise the current stream and raise if a dense attention, rotary or
-    cache call on this device reported a timeout or a bad index."""
+    cache call on this device reported a timeout or a bad index.  No call looks
+    by itself, dense_attention and its backward included: an output whose kernel
+    gave up a wait is unfinished, and only this tells.  Calls captured into a
+    graph report too if an eager one ran on the device before."""
     index = torch.device("cuda" if device is None else device).index
     index = torch.cuda.current_device() if index is None else index
     if index in _err_words:

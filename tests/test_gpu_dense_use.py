@@ -3,6 +3,8 @@ changed between the directions, captured training steps beside eager graphs,
 buffers past 32-bit offsets, and many sequences at once."""
 
 import math
+import time
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -24,6 +26,20 @@ def test_inputs_changed_before_the_backward_are_refused():
         changed += 1
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.sum().backward()
+
+
+def test_first_calls_of_two_threads_share_the_error_word(monkeypatch):
+    monkeypatch.setattr(lh.dense, "_err_words", {})
+    zeros = torch.zeros
+
+    def slow(*args, **kw):
+        time.sleep(0.3)  # both threads have found no word by now
+        return zeros(*args, **kw)
+
+    monkeypatch.setattr(torch, "zeros", slow)
+    with ThreadPoolExecutor(2) as pool:
+        a, b = pool.map(lh.dense._err, [0, 0])
+    assert a == b == lh.dense._err(0)
 
 
 def test_rotary_refuses_outputs_over_other_tensors():
