@@ -375,6 +375,8 @@ def lighthouse_attention(q, k, v, L: int, p: int, k_budget: int, chunk: int = 20
         _need(name, t, q.dtype, shape=q.shape)
     dtype = {torch.bfloat16: "bf16", torch.float32: "fp32"}[q.dtype]
     layer = Layer(B, H, N, d, L, p, k_budget, chunk, dtype, scorer, selection)
+    if rotary is None and positions is not None:
+        raise ValueError("positions: they need rotary")
     if rotary is not None:
         from .dense import apply_rotary
         q, k = apply_rotary(q, k, rotary, positions)

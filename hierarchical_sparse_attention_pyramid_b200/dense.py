@@ -475,6 +475,8 @@ def dense_attention(q, k, v, mask: AttentionMask | None = None, causal: bool = T
         raise ValueError("slopes: no gradient is computed for them")
     if rotary is not None:
         q, k = apply_rotary(q, k, rotary, positions)
+    elif positions is not None:
+        raise ValueError("positions: they need rotary")
     for_backward = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))
     return _DenseAttentionFn.apply(q, k, v, slopes, mask, for_backward,
                                    dict(causal=causal, scale=scale, softcap=softcap))

@@ -192,3 +192,12 @@ def test_python_front_end_refuses_what_it_cannot_pass():
             lh.rotary_frequencies(device="cpu", **kw)
     with pytest.raises(ValueError, match="no gradient"):
         lh.dense_attention(x, x, x, slopes=torch.zeros(2, requires_grad=True))
+
+
+def test_positions_without_rotary_are_refused():
+    x = torch.zeros(1, 2, 256, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(1, 256, dtype=torch.int32)
+    with pytest.raises(ValueError, match="positions: they need rotary"):
+        lh.dense_attention(x, x, x, positions=pos)
+    with pytest.raises(ValueError, match="positions: they need rotary"):
+        lh.lighthouse_attention(x, x, x, 1, 2, 64, positions=pos)
