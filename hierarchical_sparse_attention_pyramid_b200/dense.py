@@ -266,10 +266,10 @@ def _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts,
 class _RotaryFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, rope, positions):
-        ctx.layout, ctx.amplitude = rope.layout, rope.amplitude
+        ctx.layout, ctx.amplitude = rope.layout, float(rope.amplitude)  # one number for both directions
         ctx.save_for_backward(rope.frequencies, positions)  # changed in place before the backward: refused by torch
         q, k = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (q, k))
-        out = rotary(q, k, rope.frequencies, positions, rope.layout, rope.amplitude)
+        out = rotary(q, k, rope.frequencies, positions, rope.layout, ctx.amplitude)
         return out if k is not None else out[0]
 
     @staticmethod
@@ -282,7 +282,10 @@ class _RotaryFn(torch.autograd.Function):
 
 
 def apply_rotary(q, k, rope: Rotary, positions=None):
-    """`rotary` with its gradient.  k None: q alone (one tensor is returned)."""
+    """`rotary` with its gradient in q and k.  k None: q alone (one tensor is returned)."""
+    for name, t in (("frequencies", rope.frequencies), ("amplitude", rope.amplitude)):
+        if isinstance(t, torch.Tensor) and t.requires_grad:
+            raise ValueError(f"{name}: no gradient is computed for them")
     return _RotaryFn.apply(q, k, rope, positions)
 
 
@@ -471,8 +474,11 @@ def dense_attention(q, k, v, mask: AttentionMask | None = None, causal: bool = T
     Forward and backward may be captured in a CUDA graph.  While an eager graph of the same leaves is alive, capture
     over other ones (`q.detach().requires_grad_()`): torch makes a leaf's accumulation wait on the stream that it was
     first used on, which a capture does not allow."""
-    if slopes is not None and slopes.requires_grad:
-        raise ValueError("slopes: no gradient is computed for them")
+    for name, t in (("slopes", slopes), ("scale", scale), ("softcap", softcap)):
+        if isinstance(t, torch.Tensor) and t.requires_grad:
+            raise ValueError(f"{name}: no gradient is computed for them")
+    # read once for both directions: a tensor may hold another number by the backward
+    scale, softcap, causal = None if scale is None else float(scale), float(softcap), bool(causal)
     if rotary is not None:
         q, k = apply_rotary(q, k, rotary, positions)
     elif positions is not None:

@@ -194,6 +194,17 @@ def test_python_front_end_refuses_what_it_cannot_pass():
         lh.dense_attention(x, x, x, slopes=torch.zeros(2, requires_grad=True))
 
 
+def test_options_that_require_a_gradient_are_refused():
+    x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    one = torch.ones((), requires_grad=True)
+    f, _ = lh.rotary_frequencies(64, device="cpu")
+    for call in (lambda: lh.dense_attention(x, x, x, scale=one), lambda: lh.dense_attention(x, x, x, softcap=one),
+                 lambda: lh.apply_rotary(x, x, lh.Rotary(f.clone().requires_grad_())),
+                 lambda: lh.apply_rotary(x, x, lh.Rotary(f, amplitude=one))):
+        with pytest.raises(ValueError, match="no gradient is computed"):
+            call()
+
+
 def test_positions_without_rotary_are_refused():
     x = torch.zeros(1, 2, 256, 64, dtype=torch.bfloat16)
     pos = torch.zeros(1, 256, dtype=torch.int32)

@@ -28,6 +28,21 @@ def test_inputs_changed_before_the_backward_are_refused():
             y.sum().backward()
 
 
+def test_options_of_tensor_type_are_those_of_the_forward():
+    """Numbers given as tensors and changed before the backward: the gradient is that of the forward's numbers."""
+    def grads(change):
+        x = [randn((1, 2, 40, 64), torch.bfloat16, s).requires_grad_() for s in (1, 2, 3)]
+        scale, cap, amplitude = torch.tensor(0.125), torch.tensor(5.0), torch.tensor(1.25)
+        rope = lh.Rotary(lh.rotary_frequencies(64)[0], amplitude=amplitude)
+        y = lh.dense_attention(*x, scale=scale, softcap=cap, rotary=rope)
+        if change:
+            for t in (scale, cap, amplitude):
+                t *= 2
+        return torch.autograd.grad(y.float().square().sum(), x)
+
+    assert all(torch.equal(a, b) for a, b in zip(grads(False), grads(True)))
+
+
 def test_first_calls_of_two_threads_share_the_error_word(monkeypatch):
     monkeypatch.setattr(lh.dense, "_err_words", {})
     zeros = torch.zeros
