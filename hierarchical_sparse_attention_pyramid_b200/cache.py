@@ -93,8 +93,9 @@ def cache_write(cache: KVCache, k, v, slots) -> None:
         i2 = ctypes.c_int64 * 2
         plan = _keep(key, (k.shape[0], _lib.DENSE_DTYPES[_NAMES[k.dtype]], i2(*k.stride()[:2]), i2(*v.stride()[:2])))
     n, dtype, k_stride, v_stride = plan
-    for name, t in (("cache.k", cache.k), ("cache.v", cache.v)):
-        _writable(name, t)
+    if cache.k.requires_grad or cache.v.requires_grad:
+        _writable("cache.k", cache.k)
+        _writable("cache.v", cache.v)
     if n:
         index = cache.device.index
         _call("lh_cache_write", index, cache.ref, n, dtype, k.data_ptr(), v.data_ptr(), k_stride, v_stride,

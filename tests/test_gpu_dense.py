@@ -229,6 +229,98 @@ def test_padding_holds_anything():
             assert (got[n].transpose(1, 2)[empty] == 0).all(), n
 
 
+# More than 148 query tiles (two of them a CTA in the forward) and more than 296 key tiles (no clusters in dK/dV): what
+# the cases above stay below.
+LARGE = [
+    (2, 16, 16, 1300, 64, "fp16", 0, 0, True, 0.0, 0, 1),
+    (2, 16, 16, 1299, 128, "bf16", 1, 1, True, 20.0, 1, 0),
+    (2, 32, 16, 1281, 64, "bf16", 1, 1, True, 0.0, 0, 1),
+    (2, 32, 16, 1340, 128, "fp16", 1, 0, False, 0.0, 1, 0),
+    (3, 16, 16, 1290, 64, "bf16", 0, 0, False, 3.0, 0, 0),
+    (1, 64, 32, 1270, 128, "bf16", 1, 1, False, 0.0, 0, 1),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: "-".join(map(str, c)))
+def test_large_calls_against_fp64(case):
+    test_attention_against_fp64(case)
+
+
+@pytest.mark.parametrize("cap,alibi", [(0.0, 0), (10.0, 1)])
+@pytest.mark.parametrize("heads,d", [((16, 16), 64), ((32, 16), 128)])
+def test_padding_of_large_calls_holds_anything(heads, d, cap, alibi):
+    case = (2, *heads, 1299, d, "bf16", 1, 0, True, cap, alibi, 1)
+    q, k, v, do, _, _, slopes = dense_inputs(case)
+    ids = torch.zeros(2, 1299, dtype=torch.int32)
+    ids[0, :200] = -1   # more than a tile
+    ids[0, 350:390] = -2
+    ids[0, 390:] = 3
+    ids[0, 1250:] = -1
+    ids[1, ::7] = -1    # documents of six tokens
+    pads = (ids < 0).cuda()[:, None, :, None]
+    clean = [torch.where(pads, torch.zeros((), dtype=t.dtype, device="cuda"), t) for t in (q, k, v, do)]
+    dirty = [torch.where(pads, torch.tensor(x, dtype=t.dtype, device="cuda"), t)
+             for t, x in zip(clean, (float("nan"), float("inf"), float("nan"), float("-inf")))]
+    want = run_dense(case, (*clean, ids.cuda(), None, slopes))
+    got = run_dense(case, (*dirty, ids.cuda(), None, slopes))
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    ref = du.attention64(*clean, du.seen_matrix(2, 1299, ids, None, True, "cuda"), 1 / math.sqrt(d), cap, slopes)
+    for n in want:
+        du.check(n, got[n], ref[n])
+
+
+def test_gradients_of_a_long_row():
+    """Outputs and gradients of 65537 tokens, sampled rows, against 64 bits (the bounds of dense_util, row by row)."""
+    N, d = 65537, 64
+    q, k, v, do = (randn((1, 1, N, d), torch.bfloat16, s) for s in (1, 2, 3, 4))
+    o, saved = lh.dense_forward(q, k, v)
+    dq, dk, dv = lh.dense_backward(do, q, k, v, o, saved)
+    u, F, scale = du.half_step(torch.bfloat16), du.F, 1 / 8.0
+    rows = torch.tensor([0, 1, 127, 128, 255, 256, 40000, 65407, 65408, N - 1], device="cuda")
+    q64, k64, v64, do64 = (t[0, 0].double() for t in (q, k, v, do))
+    j = torch.arange(N, device="cuda")
+    dk64, dv64, bk, bv = (torch.zeros(len(rows), d, dtype=torch.float64, device="cuda") for _ in range(4))
+    o64, dq64, bo, bq, lse = {}, {}, {}, {}, {}
+    for i0 in range(0, N, 2048):
+        i = j[i0:i0 + 2048]
+        e = int(i[-1]) + 1
+        x = (q64[i] @ k64[:e].T * scale).masked_fill(j[:e] > i[:, None], -math.inf)
+        l64 = torch.logsumexp(x, -1)
+        p = torch.exp(x - l64[:, None])
+        del x
+        out, mag = p @ v64[:e], p @ v64[:e].abs()
+        b = u * out.abs() + (u + F) * mag
+        delta = (do64[i] * out).sum(-1, keepdim=True)
+        slack = (do64[i].abs() * b).sum(-1, keepdim=True)
+        for n, r in enumerate(rows.tolist()):
+            at = r - i0
+            if 0 <= at < len(i):
+                dp = do64[r] @ v64[:e].T
+                ds = p[at] * (dp - delta[at]) * scale
+                off = (u + F) * ds.abs() + p[at] * scale * (slack[at] + F * (do64[r].abs() @ v64[:e].abs().T))
+                o64[r], lse[r], bo[r] = out[at], l64[at], b[at]
+                dq64[r] = ds @ k64[:e]
+                bq[r] = u * dq64[r].abs() + off @ k64[:e].abs()
+        live = rows < e  # the keys that these queries reach
+        cols = rows[live]
+        pc = p[:, cols]
+        dp = do64[i] @ v64[cols].T
+        ds = pc * (dp - delta) * scale
+        off = (u + F) * ds.abs() + pc * scale * (slack + F * (do64[i].abs() @ v64[cols].abs().T))
+        dk64[live] += ds.T @ q64[i]
+        bk[live] += off.T @ q64[i].abs()
+        dv64[live] += pc.T @ do64[i]
+        bv[live] += (u + F) * (pc.T @ do64[i].abs())
+    few = 1 + 2.0 ** -5
+    pick = lambda t: torch.stack([t[r] for r in rows.tolist()])  # noqa: E731
+    du.check("o", o[0, 0, rows], (pick(o64), pick(bo) * few))
+    du.check("lse", saved.lse[0, 0, rows], (pick(lse), 2.0 ** -18 * (1 + pick(lse).abs())))
+    du.check("dq", dq[0, 0, rows], (pick(dq64), pick(bq) * few + 1e-30))
+    du.check("dk", dk[0, 0, rows], (dk64, (u * dk64.abs() + bk) * few + 1e-30))
+    du.check("dv", dv[0, 0, rows], (dv64, (u * dv64.abs() + bv) * few + 1e-30))
+
+
 def test_scores_of_the_lowest_values():
     """Keys that give scores of -1e30 beside others, and rows whose only keys do."""
     q, k, v = (torch.ones(1, 1, 130, 64, dtype=torch.bfloat16, device="cuda") for _ in range(3))
@@ -377,6 +469,29 @@ def test_rotary_in_the_layer_and_the_dense_attention():
     ref = du.attention64(qr, kr, v, torch.zeros_like(v), seen, 1 / 8.0)["o"]
     du.check("dense", z, ref)
     du.check("layer", y, ref)
+
+
+def test_gradient_through_the_layer_with_rotary():
+    """lighthouse_attention(rotary=): the gradients are the layer's on the turned inputs, turned back."""
+    q, k, v, g = (randn((1, 2, 512, 64), torch.bfloat16, s) for s in (1, 2, 3, 4))
+    rope = lh.Rotary.make(32, layout="interleaved", scaling="linear", factor=2.0)
+    pos = torch.randint(0, 100000, (1, 512), dtype=torch.int32, device="cuda")
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+    y = lh.lighthouse_attention(*x, 3, 2, 64, rotary=rope, positions=pos)
+    y.backward(g)
+    turned = [t.detach().requires_grad_() for t in (*lh.rotary(q, k, rope.frequencies, pos, "interleaved"), v)]
+    z = lh.lighthouse_attention(*turned, 3, 2, 64)
+    z.backward(g)
+    assert torch.equal(y, z)
+    back = lh.rotary(turned[0].grad, turned[1].grad, rope.frequencies, pos, "interleaved", inverse=True)
+    for a, b in zip(x, (*back, turned[2].grad)):
+        assert torch.equal(a.grad, b)
+    # and those of the formula: with one level the layer is causal attention
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+    lh.lighthouse_attention(*x, 1, 2, 64, rotary=rope, positions=pos).backward(g)
+    qr, kr = lh.rotary(q, k, rope.frequencies, pos, "interleaved")
+    ref = du.attention64(qr, kr, v, g, du.seen_matrix(1, 512, device="cuda"), 1 / 8.0)
+    du.check("dv", x[2].grad, ref["dv"])
 
 
 def test_streams_and_graphs():
