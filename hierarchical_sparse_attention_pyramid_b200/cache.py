@@ -156,10 +156,11 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
         _not_tensors(q=q, page_table=page_table, lens=lens, q_start=q_start, tree_mask=tree_mask, slopes=slopes)
         raise
     plan = _plans.get(key)
-    if plan is None:
+    fresh = plan is None
+    if fresh:
         _are_tensors(q=q, page_table=page_table, lens=lens)
         cfg = _attention_config(cache, q, page_table, lens, q_start, max_tokens, tree_mask, scale, softcap, slopes)
-        plan = _keep(key, (cfg, _lib.load().lh_cache_attn_ws_bytes(cache.ref, cfg)))
+        plan = cfg, _lib.load().lh_cache_attn_ws_bytes(cache.ref, cfg)
     cfg, need = plan
     if out is None:
         out = _contiguous_like(q)
@@ -171,6 +172,8 @@ def cache_attention(cache: KVCache, q, page_table, lens, q_start=None, max_token
     index = cache.device.index
     _call("lh_cache_attn", index, cache.ref, cfg, q.data_ptr(), page_table.data_ptr(), lens.data_ptr(), _ptr(q_start),
           _ptr(tree_mask), _ptr(slopes), out.data_ptr(), _ptr(ws), need, _err(index))
+    if fresh:
+        _keep(key, plan)  # of a call that it refuses (by a pointer) the library gives no size
     return out
 
 

@@ -270,6 +270,19 @@ def test_padding_of_large_calls_holds_anything(heads, d, cap, alibi):
         du.check(n, got[n], ref[n])
 
 
+@pytest.mark.parametrize("N", [90, 700])
+def test_backward_without_what_rounding_took_off(N):
+    """for_backward False: row sums from the rounded output, within the same bounds (they count its rounding)."""
+    case = (2, 4, 2, N, 64, "bf16", 1, 1, True, 20.0, 0, 1)
+    q, k, v, do, ids, pre, _ = dense_inputs(case)
+    opt = dict(mask=lh.attention_mask(ids, pre), softcap=20.0)
+    o, saved = lh.dense_forward(q, k, v, for_backward=False, **opt)
+    assert saved.o_low is None
+    ref = du.attention64(q, k, v, do, du.seen_matrix(2, N, ids, pre, True, "cuda"), 1 / 8.0, 20.0)
+    for n, got in zip(("o", "dq", "dk", "dv"), (o, *lh.dense_backward(do, q, k, v, o, saved, **opt))):
+        du.check(n, got, ref[n])
+
+
 def test_gradients_of_a_long_row():
     """Outputs and gradients of 65537 tokens, sampled rows, against 64 bits (the bounds of dense_util, row by row)."""
     N, d = 65537, 64

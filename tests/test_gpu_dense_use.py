@@ -57,6 +57,19 @@ def test_first_calls_of_two_threads_share_the_error_word(monkeypatch):
     assert a == b == lh.dense._err(0)
 
 
+def test_a_refused_call_leaves_no_plan():
+    """A cache at an address that the library refuses, then one of the same shapes that it takes."""
+    lens = (300, 40)
+    cache, table, ks, vs = filled("bf16", lens, 2, 64, 32)
+    q = randn((2, 6, 64), torch.bfloat16, 5)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    odd = torch.zeros(cache.k.numel() + 4, dtype=torch.bfloat16, device="cuda")[4:].view(cache.k.shape)
+    with pytest.raises(lh._lib.LhError, match="16-byte"):
+        lh.cache_attention(lh.KVCache(odd, cache.v), q, table, ln)
+    got = lh.cache_attention(cache, q, table, ln)
+    du.check("o", got, du.cache_attention64(q, ks, vs, [0, 1, 2], lens))
+
+
 def test_rotary_refuses_outputs_over_other_tensors():
     q, k = randn((1, 2, 6, 64), torch.bfloat16, 1), randn((1, 2, 6, 64), torch.bfloat16, 2)
     f, _ = lh.rotary_frequencies(64)
