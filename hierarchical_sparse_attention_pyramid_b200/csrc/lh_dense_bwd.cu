@@ -5,8 +5,9 @@
 // the derivative of the cap; 1 without one).
 //
 // Two kernels, each writing its gradients once, so that no sum depends on the
-// order in which CTAs finish (a single kernel would add dQ with atomics for
-// 5 instead of 7 matrix products a tile):
+// order in which CTAs finish (a single kernel, 5 instead of 7 matrix products a
+// tile, would add dQ up across CTAs, in any order by atomics or in a fixed one
+// by waiting for turns; the latter has not been built):
 //
 // dense_bwd_q_kernel (Delta, dQ) - one CTA per 128-query tile and query head;
 //   S = Q K_j^T runs two key tiles ahead into a double-buffered TMEM region

@@ -504,7 +504,8 @@ typedef struct {
  * exponentials; o_low [B][Hq][N][d] in the inputs' type, contiguous, or NULL:
  * what rounding to o took off (for lh_dense_bwd).  A query without keys, or whose scores are all -inf, has O = 0 and
  * LSE = -inf; one that sees a score of NaN or +inf is NaN.
- * Probabilities enter P V rounded to the inputs' type; sums are fp32.  Values
+ * Probabilities enter P V rounded to the inputs' type; sums are fp32.  Without cap and slopes a quarter of the
+ * exponentials of unmasked tiles come from a polynomial (4e-6 relative), which LSE shows.  Values
  * in padding and past N are not used; those of another document of the batch
  * row must be finite. */
 lh_status lh_dense_fwd(const lh_dense_config *cfg, const void *q, const void *k, const void *v, const void *spans,
@@ -576,8 +577,14 @@ typedef struct {
  * of its mask is set.  Formulas as lh_dense_fwd (slopes: distances between
  * positions; not together with a tree).
  * Out: o [n_tok][Hq][d] of dtype, contiguous; 0 where a token sees nothing;
- * tokens of no sequence are left as they are.  ws: lh_cache_attn_ws_bytes
- * bytes of scratch (its contents before and after do not matter; NULL when 0).
+ * tokens of no sequence are left as they are.  Probabilities enter P V in the
+ * operands' 16 bits: bf16 over a bf16 cache, else fp16, whose steps below 2^-14
+ * of a row's largest are 2^-24 of it.  Over 8-bit kinds they are multiplied by
+ * their value's scale relative to the largest scale met, in steps of 2^-30 of
+ * the two largest together (a value 2^20 smaller than the largest loses bits of
+ * its weight), and bf16 queries become fp16 (exact down to 2^-28 of a row's
+ * largest).  ws: lh_cache_attn_ws_bytes bytes of scratch (its contents before
+ * and after do not matter; NULL when 0).
  * Lengths and tables that do not fit (a page outside the cache, a length past
  * the table, more than max_tokens tokens) are cut to what does and set the
  * error word's bounds bit.  What the cache holds past a sequence's length is
