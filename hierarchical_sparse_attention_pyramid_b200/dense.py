@@ -220,7 +220,7 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
         for i, o in enumerate(outs):
             _writable(f"out[{i}]", o)
             for j, t in enumerate(ts + tuple(outs[:i])):  # the calls' own check: what begins at one place
-                if o.data_ptr() == t.data_ptr() and o.numel() and (i != j or o.stride() != t.stride()):
+                if o.data_ptr() == t.data_ptr() and o.numel() and (i != j or not _same_places(o, t)):
                     raise ValueError(f"out[{i}]: overlaps another tensor of the call")
     cfg = _plans.get(key)
     if cfg is None:
@@ -231,6 +231,11 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
         if out is not None:
             _written(outs)
     return outs[0], (outs[1] if k is not None else None)
+
+
+def _same_places(a, b) -> bool:
+    """Of two tensors that begin at one place: whether an index is the same place in both."""
+    return a.shape == b.shape and all(n == 1 or s == t for n, s, t in zip(a.shape, a.stride(), b.stride()))
 
 
 def _rotary_config(q, k, frequencies, positions, layout, amplitude, inverse, ts, outs):

@@ -82,6 +82,11 @@ def test_rotary_refuses_outputs_over_other_tensors():
         lh.rotary(q, None, f, out=(q.view(1, 6, 2, 64).transpose(1, 2),))
     lh.rotary(q, k, f, out=(q, k))
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    # in place, by a view whose strides differ only where there is one index
+    one = randn((3, 1, 2, 64), torch.bfloat16, 4)
+    want = lh.rotary(one.transpose(1, 2), None, f)[0]
+    lh.rotary(one.transpose(1, 2), None, f, out=(one.view(3, 2, 1, 64),))
+    assert torch.equal(one.transpose(1, 2), want)
     # the same tensor for both, turned into two others
     a, b = lh.rotary(q, q, f)
     assert torch.equal(a, b)
